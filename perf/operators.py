@@ -142,7 +142,8 @@ def _tiled_ragged(scales, offsets):
     to = torch.cumsum(padded, 0) - padded
     rows = torch.arange(scales.shape[0], device=scales.device)
     g = torch.searchsorted(at[1:], rows, right=True)
-    s = scales.new_zeros((max(256, int(padded.sum())), scales.shape[1]))
+    M, G = scales.shape[0], at.shape[0] - 1
+    s = scales.new_zeros((256 * (M // 256 + min(M, G)), scales.shape[1]))  # room for any lengths of the groups
     s[to[g] + rows - at[g]] = scales
     return _tiled(s[None])
 
