@@ -360,6 +360,92 @@ void* moe_pipeline_stream(const moe_pipeline* p, int which);
 moe_status moe_pipeline_destroy(moe_pipeline* p);
 
 /*
+ * MXFP4 (OCP microscaling formats, "MX"): a matrix [rows, cols] as
+ *   codes   uint8 [rows, cols / 2]: E2M1 elements (0, 0.5, 1, 1.5, 2, 3, 4, 6
+ *           and their negatives), element 2i in the low, 2i + 1 in the high
+ *           half of byte i of a row;
+ *   scales  one E8M0 byte (2^(byte - 127); 0xFF: NaN) per 32 columns, in tiles
+ *           of 128 rows x 128 columns: with stages = ceil(cols / 256) and row r
+ *           of tile row q, the byte of column block b stands at
+ *             (q * stages + b / 8) * 1024 + (b / 4 % 2) * 512
+ *             + (r % 32) * 16 + (r / 32) * 4 + b % 4.
+ *           Every group of rows (an expert) begins at an even tile row, so it
+ *           takes 2 * ceil(rows / 256) of them. Bytes of columns behind the
+ *           last one are 0 where a row has them; those of rows behind a
+ *           group's last are unspecified.
+ * Columns are a multiple of 32. Groups are either dense, [groups, rows, cols]
+ * with `rows` each (offsets NULL), or rows in all with group g at rows
+ * offsets[g] .. offsets[g + 1] - 1 (device int32 [groups + 1], not decreasing,
+ * groups <= 256; rows of no group are neither read nor written). Group g then
+ * begins at tile row sum over g' < g of 2 * ceil(rows of g' / 256).
+ */
+
+/* Bytes of scales of a matrix of `groups` dense groups of `rows` rows each, or
+ * (ragged != 0) of `rows` rows in `groups` groups of any lengths. 0: invalid. */
+size_t moe_mx_scale_bytes(int groups, int rows, int cols, int ragged);
+
+/*
+ * moe_mx_quantize — x (fp32 or bf16, row-major, 16-byte aligned) to MXFP4:
+ * the scale of a block is 2^s, s = max(floor(log2(largest magnitude)) - 2,
+ * -127), and each element x / 2^s rounded to the nearest code (ties to even,
+ * beyond 6 to 6). A block with a NaN or an infinity gets the scale NaN.
+ * moe_mx_dequantize — the values back (exact in both types).
+ */
+moe_status moe_mx_quantize(const void* x, const int32_t* offsets, int groups, int rows, int cols, moe_dtype dtype,
+                           void* data, void* scales, size_t scale_bytes, void* stream);
+moe_status moe_mx_dequantize(const void* data, const void* scales, size_t scale_bytes, const int32_t* offsets,
+                             int groups, int rows, int cols, moe_dtype dtype, void* out, void* stream);
+
+/*
+ * moe_mx_matmul — out[r, :] = A[r] . B[g]^T for the rows r of every group g:
+ * A [groups, M, K] (offsets NULL) or [M, K] with offsets, B [groups, N, K]
+ * dense, both MXFP4, out [rows of A, N] fp32 or bf16. Products and sums in
+ * fp32, rounded once. N % 8 == 0, groups <= 256. Rows of no group are left as
+ * they were. The scales of A and B hold moe_mx_scale_bytes() bytes.
+ * status_dev: device int32 [1], required: MOE_DEV_INTERNAL is OR-ed in and
+ * nothing computed when the offsets are not a partition (negative, decreasing
+ * or past M).
+ */
+moe_status moe_mx_matmul(const void* a, const void* a_scales, const void* b, const void* b_scales,
+                         const int32_t* offsets, int groups, int M, int N, int K, moe_dtype out_dtype, void* out,
+                         int32_t* status_dev, void* stream);
+
+/*
+ * The layer with its experts in MXFP4: x is rounded to MXFP4 row by row (the
+ * router sees x itself), both products of an expert multiply MXFP4 matrices,
+ * and the SwiGLU hidden rows are rounded to MXFP4 from fp32 between them. Each
+ * expert row times its gate is rounded to bf16, a token's rows are added in
+ * slot order in fp32, and out [T, d] is bf16. d % 32 == 0 and I % 32 == 0.
+ *
+ * moe_mx_experts takes the choices and gates: topk_idx [T, k], any experts
+ * (the same one twice is two assignments), topk_gate [T, k] any values. A
+ * choice outside [0, E) sets MOE_DEV_INTERNAL and adds nothing. counts [E] may
+ * be NULL.
+ * moe_mx_forward runs the router before them; arguments and outputs as for
+ * moe_forward (x and w_router in `dtype`, with the limits of its router).
+ * workspace: moe_mx_workspace_size() bytes, 256-byte aligned, any contents.
+ * Results are bit-identical from run to run.
+ */
+typedef struct moe_mx_weights {
+  size_t struct_bytes;      /* sizeof(moe_mx_weights) */
+  const void* gate;         /* codes  [E, I, d / 2] */
+  const void* gate_scales;  /* scales of E groups of I rows, d columns */
+  const void* up;           /* as gate */
+  const void* up_scales;
+  const void* down;         /* codes  [E, d, I / 2] */
+  const void* down_scales;  /* scales of E groups of d rows, I columns */
+} moe_mx_weights;
+
+size_t moe_mx_workspace_size(int T, int d, int E, int k, int I);
+moe_status moe_mx_experts(const void* x, const int32_t* topk_idx, const float* topk_gate, const moe_mx_weights* w,
+                          int T, int d, int E, int k, int I, moe_dtype dtype, void* out, int32_t* counts,
+                          void* workspace, size_t workspace_bytes, int32_t* status_dev, void* stream);
+moe_status moe_mx_forward(const void* x, const void* w_router, const float* b_router, const moe_mx_weights* w, int T,
+                          int d, int E, int k, int I, int renorm, moe_dtype dtype, void* out, int32_t* topk_idx,
+                          float* topk_gate, int32_t* counts, float* aux, void* workspace, size_t workspace_bytes,
+                          int32_t* status_dev, void* stream);
+
+/*
  * moe_selftest_wait_timeout — a diagnostic of the failure handling every
  * kernel of the library shares: it launches one warp on `stream` that waits
  * on a shared-memory barrier phase nothing will complete, through the same

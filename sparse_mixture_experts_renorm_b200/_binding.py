@@ -28,7 +28,9 @@ STATUS_NAMES = {
 EXPORTED = ("moe_workspace_size", "moe_forward", "moe_forward_events", "moe_kernel_name", "moe_get_permutation",
             "moe_last_error_detail", "moe_forward_noalloc", "moe_selftest_wait_timeout", "moe_workspace_size_ex",
             "moe_forward_ex", "moe_launch_plan", "moe_pipeline_create", "moe_pipeline_submit",
-            "moe_pipeline_synchronize", "moe_pipeline_stream", "moe_pipeline_destroy")
+            "moe_pipeline_synchronize", "moe_pipeline_stream", "moe_pipeline_destroy", "moe_mx_scale_bytes",
+            "moe_mx_quantize", "moe_mx_dequantize", "moe_mx_matmul", "moe_mx_workspace_size", "moe_mx_experts",
+            "moe_mx_forward")
 MOE_NORM_NONE, MOE_NORM_RMS, MOE_NORM_RMS_EPS_OUTSIDE = 0, 1, 2
 MOE_MAX_SHARED = 8
 MOE_NOALLOC_SCRATCH_BYTES = 16 << 20
@@ -82,6 +84,20 @@ class moe_layer_desc(ctypes.Structure):
         ("x_dev", ctypes.c_void_p * 2),
         ("out_dev", ctypes.c_void_p * 2),
         ("aux_dev", ctypes.c_void_p * 2),
+    ]
+
+
+class moe_mx_weights(ctypes.Structure):
+    """The C struct ``moe_mx_weights`` of include/moe.h (same field order and types)."""
+
+    _fields_ = [
+        ("struct_bytes", ctypes.c_size_t),
+        ("gate", ctypes.c_void_p),
+        ("gate_scales", ctypes.c_void_p),
+        ("up", ctypes.c_void_p),
+        ("up_scales", ctypes.c_void_p),
+        ("down", ctypes.c_void_p),
+        ("down_scales", ctypes.c_void_p),
     ]
 
 
@@ -140,6 +156,21 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.moe_selftest_wait_timeout.restype = I32
     lib.moe_get_permutation.argtypes = [P, SZ, I32, I32, I32, I32, I32, I32, P, P, P, P]
     lib.moe_get_permutation.restype = I32
+    lib.moe_mx_scale_bytes.argtypes = [I32, I32, I32, I32]
+    lib.moe_mx_scale_bytes.restype = SZ
+    lib.moe_mx_quantize.argtypes = [P, P, I32, I32, I32, I32, P, P, SZ, P]
+    lib.moe_mx_quantize.restype = I32
+    lib.moe_mx_dequantize.argtypes = [P, P, SZ, P, I32, I32, I32, I32, P, P]
+    lib.moe_mx_dequantize.restype = I32
+    lib.moe_mx_matmul.argtypes = [P, P, P, P, P, I32, I32, I32, I32, I32, P, P, P]
+    lib.moe_mx_matmul.restype = I32
+    MXW = ctypes.POINTER(moe_mx_weights)
+    lib.moe_mx_workspace_size.argtypes = [I32, I32, I32, I32, I32]
+    lib.moe_mx_workspace_size.restype = SZ
+    lib.moe_mx_experts.argtypes = [P, P, P, MXW, I32, I32, I32, I32, I32, I32, P, P, P, SZ, P, P]
+    lib.moe_mx_experts.restype = I32
+    lib.moe_mx_forward.argtypes = [P, P, P, MXW, I32, I32, I32, I32, I32, I32, I32, P, P, P, P, P, P, SZ, P, P]
+    lib.moe_mx_forward.restype = I32
     lib.moe_last_error_detail.argtypes = [ctypes.c_char_p, SZ]
     lib.moe_last_error_detail.restype = SZ
     if path is None:

@@ -13,11 +13,11 @@
 #include <string>
 
 #include "moe_internal.h"
+#include "mx_internal.h"
 
 namespace moe {
-namespace {
 
-thread_local std::string g_last_error;
+static thread_local std::string g_last_error;
 
 moe_status fail(moe_status st, const char* fmt, ...) {
   char buf[512];
@@ -32,10 +32,6 @@ moe_status fail(moe_status st, const char* fmt, ...) {
 moe_status fail_cuda(cudaError_t err, const char* what) {
   return fail(MOE_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(err), cudaGetErrorString(err));
 }
-
-size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Shape checks shared by every entry point.
 moe_status check_shape(int T, int d, int E, int k, int I, moe_dtype dtype) {
@@ -61,7 +57,7 @@ moe_status check_shape(int T, int d, int E, int k, int I, moe_dtype dtype) {
   return MOE_OK;
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 get_encode_fn() {
+static PFN_cuTensorMapEncodeTiled_v12000 get_encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
   std::call_once(once, [] {
@@ -73,8 +69,6 @@ PFN_cuTensorMapEncodeTiled_v12000 get_encode_fn() {
   });
   return fn;
 }
-
-}  // namespace
 
 void set_error_detail(const char* fmt, ...) {
   char buf[512];
@@ -131,6 +125,30 @@ bool make_tmap_bf16_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64
                       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
+}
+
+bool make_tmap_mx_codes(CUtensorMap* map, const void* base, uint64_t rows, uint64_t row_bytes) {
+  PFN_cuTensorMapEncodeTiled_v12000 encode = get_encode_fn();
+  if (!encode) return false;
+  cuuint64_t dims[2] = {row_bytes, rows};
+  cuuint64_t strides[1] = {row_bytes};
+  cuuint32_t box[2] = {128, 128};
+  cuuint32_t estr[2] = {1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool make_tmap_mx_scales(CUtensorMap* map, const void* base, uint64_t rows) {
+  PFN_cuTensorMapEncodeTiled_v12000 encode = get_encode_fn();
+  if (!encode) return false;
+  cuuint64_t dims[2] = {256, rows};  // 32-bit words: an inner box has at most 256 elements
+  cuuint64_t strides[1] = {1024};
+  cuuint32_t box[2] = {256, 1};
+  cuuint32_t estr[2] = {1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(base), dims, strides, box, estr,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace moe

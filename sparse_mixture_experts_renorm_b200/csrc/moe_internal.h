@@ -90,8 +90,17 @@ struct RouterNorm {
 
 Workspace workspace_layout(int T, int d, int E, int k, int I, moe_dtype dtype, int n_shared = 0, bool norm = false);
 
-// Sets the calling thread's moe_last_error_detail() message (printf format).
+// Sets the calling thread's moe_last_error_detail() message (printf format);
+// fail() also returns the status.
 void set_error_detail(const char* fmt, ...);
+moe_status fail(moe_status st, const char* fmt, ...);
+moe_status fail_cuda(cudaError_t err, const char* what);
+
+// Shape checks shared by the layer's entry points.
+moe_status check_shape(int T, int d, int E, int k, int I, moe_dtype dtype);
+
+inline size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 inline int router_block_tokens(moe_dtype dtype) { return dtype == MOE_BF16 ? kRouterTokensTc : kRouterTokensSimt; }
 inline int router_blocks(int T, moe_dtype dtype) {

@@ -1,0 +1,449 @@
+// mx_gemm.cu — grouped products of MXFP4 matrices on block-scaled tcgen05
+// (kind::mxf4) with a pair of CTAs (cta_group::2) per 256 x 256 tile.
+//
+//   product:  out[r, n] = g_r * sum_k A[r, k] B[e(r), n, k]
+//   gate/up:  H[r, i]   = MXFP4( SiLU(A[r] . Wg[e, i]) * (A[r] . Wu[e, i]) )
+//
+// for the rows r of group e (an expert's dispatched rows). The tensor cores
+// multiply E2M1 codes exactly, apply the two E8M0 scales of every 32 products
+// and add in fp32, so nothing is rounded before the epilogue.
+//
+// Rows are the UMMA M operand (128 per CTA), weight rows the N operand (128
+// staged by each CTA; for gate/up CTA 0 stages the gate rows of the block's
+// 128 hidden units and CTA 1 their up rows, so a TMEM lane holds one row's
+// gate values in columns 0-127 and its up values in 128-255, and neither
+// SwiGLU nor the quantisation of H leaves the thread). A pipeline stage is 256
+// columns of K: 128 bytes of codes a row with the 128-byte swizzle, as for 64
+// bf16, and 1024 bytes of scales per 128 rows, which one thread copies to TMEM
+// (tcgen05.cp) in front of the stage's four UMMAs. Both CTAs need the scales
+// of all 256 weight rows. 35 KB a stage, 6 stages.
+//
+// TMEM: the accumulator takes 256 of 512 columns, the scales 32 columns for
+// each of 4 rotating buffers, so there is no room for a second accumulator of
+// 256 columns. Instead eight epilogue warps first bring their 128 columns into
+// registers and release the accumulator, then do the arithmetic and the stores
+// while the next tile's UMMAs run.
+//
+// Persistent: clusters walk the tiles (groups in order, weight block outer,
+// row tile inner). Every wait is bounded.
+#include <atomic>
+
+#include "mx.cuh"
+#include "mx_internal.h"
+#include "pair.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kMxStages = 6;
+constexpr int kMxEpiWarps = 8;
+constexpr int kMxThreads = 64 + 32 * kMxEpiWarps;
+constexpr int kHalf = 128 * 128;                // 128 rows x 256 codes
+constexpr int kSfBytes = 3 * kMxStageBytes;     // scales of 128 rows, and of 256 weight rows
+constexpr int kMxSmem = kMxStages * (2 * kHalf + kSfBytes) + 1024 + 4096;
+constexpr uint32_t kStageTx = 2u * (2 * kHalf + kSfBytes);  // both CTAs
+constexpr uint32_t kSfCol = 256;                // first TMEM column of the scales
+constexpr int kSfBufs = 4, kSfCols = 32;
+static_assert(kMxSmem <= 227 * 1024, "shared memory");
+
+// Instruction descriptor for kind::mxf4 (E2M1 x E2M1, E8M0 scales, fp32
+// accumulator, both operands K-major): B scale id in bits [4,6), A format 1 =
+// E2M1 in [7,10), B format 1 in [10,12), N >> 3 in [17,23), scale format 1 =
+// E8M0 in bit 23, M >> 7 in [27,29), A scale id in [29,31).
+__device__ constexpr uint32_t idesc_mxf4(int M, int N, uint32_t sf_id) {
+  return (sf_id << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) | (1u << 23) |
+         (static_cast<uint32_t>(M >> 7) << 27) | (sf_id << 29);
+}
+
+// D[tmem] (+)= A * B^T, 64 columns of K, one scale per 32 of them.
+__device__ __forceinline__ void tc_mma_mxf4_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                                 uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+          d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+
+// 512 bytes of scales (128 rows x 4) from both CTAs' shared memory to four
+// columns of their own TMEM, repeated in every lane quarter.
+__device__ __forceinline__ void tc_cp_scales_pair(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+// Matrix descriptor of a 32 x 16-byte tile without swizzle: 8-row core
+// matrices of 128 bytes one after the other.
+__device__ __forceinline__ uint64_t scales_desc(uint32_t smem_addr) {
+  uint64_t desc = 0;
+  desc |= static_cast<uint64_t>((smem_addr & 0x3FFFFu) >> 4);
+  desc |= static_cast<uint64_t>(16u >> 4) << 16;
+  desc |= static_cast<uint64_t>(128u >> 4) << 32;
+  desc |= static_cast<uint64_t>(1u) << 46;
+  return desc;
+}
+
+struct MxTile {
+  int g, m, n, row0, cnt;  // group, 256-row tile, weight block, first row and rows of the group
+};
+
+__device__ __forceinline__ MxTile mx_tile(int tile, int n_wb, const int* s_off, const int* s_mt, int G) {
+  const int q = tile / n_wb;
+  int lo = 0, hi = G;  // s_mt[lo] <= q < s_mt[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (s_mt[mid] <= q)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  MxTile t;
+  t.g = lo;
+  const int mt = s_mt[lo + 1] - s_mt[lo];
+  const int local = tile - s_mt[lo] * n_wb;
+  t.n = local / mt;
+  t.m = local - t.n * mt;
+  t.row0 = s_off[lo];
+  t.cnt = s_off[lo + 1] - s_off[lo];
+  return t;
+}
+
+// kGateUp: see above. Maps: codes of A and of the weights (boxes of 128 rows x
+// 128 bytes), scales of A and of the weights (boxes of 1024 bytes). For the
+// product tmB1/tmSB1 repeat tmB0/tmSB0.
+template <bool kGateUp>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
+    mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmSA,
+                   const __grid_constant__ CUtensorMap tmB0, const __grid_constant__ CUtensorMap tmB1,
+                   const __grid_constant__ CUtensorMap tmSB0, const __grid_constant__ CUtensorMap tmSB1,
+                   const int32_t* __restrict__ offsets, int G, int M, int N, int K, int group_tiles,
+                   const MxOut out, int32_t* status, uint64_t limit_ns) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sA = smem;
+  uint8_t* sB = smem + kMxStages * kHalf;
+  uint8_t* sS = smem + 2 * kMxStages * kHalf;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kMxStages * (2 * kHalf + kSfBytes));
+  uint64_t* full = bars;               // leader: the stage's bytes of both CTAs
+  uint64_t* empty = bars + kMxStages;  // both: stage consumed by the pair's UMMAs
+  uint64_t* tfull = bars + 2 * kMxStages;
+  uint64_t* tempty = tfull + 1;        // leader: the epilogue threads of both CTAs
+  uint64_t* done = tempty + 1;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(done + 1);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
+  int* s_bad = reinterpret_cast<int*>(s_tmem + 2);
+  int* s_off = reinterpret_cast<int*>(s_tmem + 4);  // [G + 1]
+  int* s_mt = s_off + kMaxExperts + 1;              // [G + 1]
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int cid = (int)cluster_id_x();
+  const int ncl = (int)num_clusters_x();
+  const int n_wb = kGateUp ? (N + 127) / 128 : (N + 255) / 256;
+  const int KB = mx_stages(K);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kMxStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(tfull, 1);
+    mbar_init(tempty, 2 * 32 * kMxEpiWarps);
+    mbar_init(done, 1);
+    *s_abort = 0;
+    *s_bad = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(s_tmem, 512);
+    tmem_relinquish_pair();
+  }
+  pdl_wait();
+  __syncthreads();
+  // the groups' rows and the prefix of their 256-row tiles
+  for (int i = threadIdx.x; i <= G; i += blockDim.x) {
+    const int o = offsets ? offsets[i] : i * M;
+    s_off[i] = o;
+    const int next = i < G ? (offsets ? offsets[i + 1] : (i + 1) * M) : o;
+    if (o < 0 || next < o || (offsets && next > M)) *s_bad = 1;
+  }
+  __syncthreads();
+  if (*s_bad) {  // not a partition of the rows: nothing is computed
+    if (threadIdx.x == 0) atomicOr(status, MOE_DEV_INTERNAL);
+  }
+  if (warp == 0) {
+    int run = 0;
+    for (int g0 = 0; g0 < G; g0 += 32) {
+      const int g = g0 + lane;
+      const int t = (g < G && !*s_bad) ? (s_off[g + 1] - s_off[g] + 255) >> 8 : 0;
+      int incl = t;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int n = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += n;
+      }
+      if (g < G) s_mt[g] = run + incl - t;
+      run += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) s_mt[G] = run;
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // the peer's barriers are initialised before any remote signal
+  tc_fence_after();
+  const uint32_t tmem_base = *s_tmem;
+  const int total = s_mt[G] * n_wb;
+
+  if (warp == 0) {
+    // ------------------------------------------------------ TMA producer --
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      int issued = 0;
+      bool ok = true;
+      for (int tile = cid; ok && tile < total; tile += ncl) {
+        const MxTile t = mx_tile(tile, n_wb, s_off, s_mt, G);
+        const int arow = t.row0 + t.m * 256 + (int)rank * 128;
+        const int asf = (2 * (s_mt[t.g] + t.m) + (int)rank) * KB;
+        // gate/up: rank 0 stages the gate rows, rank 1 the up rows
+        const int brow = kGateUp ? t.g * N + t.n * 128 : t.g * N + t.n * 256 + (int)rank * 128;
+        const CUtensorMap* mB = kGateUp && rank ? &tmB1 : &tmB0;
+        const int bsf0 = (t.g * group_tiles + (kGateUp ? t.n : 2 * t.n)) * KB;
+        const int bsf1 = kGateUp ? bsf0 : bsf0 + KB;
+        for (int kb = 0; kb < KB; ++kb) {
+          if (!mbar_wait(&empty[stage], phase ^ 1u, s_abort, status, limit_ns)) {
+            ok = false;
+            break;
+          }
+          const uint32_t fbar = map_to_cta(&full[stage], 0);
+          if (leader) mbar_arrive_expect_tx(&full[stage], kStageTx);
+          uint8_t* ss = sS + stage * kSfBytes;
+          tma_load_2d_pair(sA + stage * kHalf, &tmA, fbar, kb * 128, arow);
+          tma_load_2d_pair(sB + stage * kHalf, mB, fbar, kb * 128, brow);
+          tma_load_2d_pair(ss, &tmSA, fbar, 0, asf + kb);
+          tma_load_2d_pair(ss + kMxStageBytes, &tmSB0, fbar, 0, bsf0 + kb);
+          tma_load_2d_pair(ss + 2 * kMxStageBytes, &tmSB1, fbar, 0, bsf1 + kb);
+          ++issued;
+          if (++stage == kMxStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // loads land on the leader's barriers: it waits for the last phase of
+      // each stage it armed (these cover both CTAs' bytes)
+      if (leader) {
+        const int n = issued < kMxStages ? issued : kMxStages;
+        for (int i = 0; i < n; ++i) {
+          if (stage == 0) {
+            stage = kMxStages;
+            phase ^= 1u;
+          }
+          --stage;
+          mbar_wait(&full[stage], phase, nullptr, status, limit_ns);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------ MMA issuer (leader only) --
+    if (leader && lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      uint32_t acc_phase = 0;
+      int buf = 0;
+      bool ok = true;
+      for (int tile = cid; ok && tile < total; tile += ncl) {
+        if (!mbar_wait(tempty, acc_phase ^ 1u, s_abort, status, limit_ns)) break;
+        tc_fence_after();
+        for (int kb = 0; kb < KB; ++kb) {
+          if (!mbar_wait(&full[stage], phase, s_abort, status, limit_ns)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t ss = smem_u32(sS + stage * kSfBytes);
+          const uint32_t sf = tmem_base + kSfCol + static_cast<uint32_t>(buf * kSfCols);
+          const int steps = min(4, (K - kb * kMxStageCols + 63) >> 6);  // 64 columns each
+          // columns: A's two tiles at 0 and 4, B's two at 8 and 16 (eight
+          // columns: the scales of 2 x 128 weight rows)
+          for (int t = 0; t < (steps + 1) >> 1; ++t) {
+            tc_cp_scales_pair(sf + 4 * t, scales_desc(ss + 512 * t));
+            tc_cp_scales_pair(sf + 8 + 8 * t, scales_desc(ss + kMxStageBytes + 512 * t));
+            tc_cp_scales_pair(sf + 12 + 8 * t, scales_desc(ss + 2 * kMxStageBytes + 512 * t));
+          }
+          const uint64_t adesc = sw128_kmajor_desc(smem_u32(sA + stage * kHalf));
+          const uint64_t bdesc = sw128_kmajor_desc(smem_u32(sB + stage * kHalf));
+          for (int s = 0; s < steps; ++s)
+            tc_mma_mxf4_pair(tmem_base, adesc + static_cast<uint64_t>(s * 2), bdesc + static_cast<uint64_t>(s * 2),
+                             idesc_mxf4(256, 256, s & 1 ? 2u : 0u), sf + 4 * (s >> 1), sf + 8 + 8 * (s >> 1),
+                             (kb | s) != 0 ? 1u : 0u);
+          tc_commit_pair_both(&empty[stage]);
+          buf = (buf + 1) & (kSfBufs - 1);
+          if (++stage == kMxStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        tc_commit_pair_both(tfull);
+        acc_phase ^= 1u;
+      }
+      tc_commit_pair_local(done);
+      mbar_wait(done, 0, nullptr, status, limit_ns);
+    }
+    __syncwarp();
+  } else {
+    // --------------------------------------------------------- epilogue --
+    // TMEM lane = a row of this CTA's half of the tile. The two groups of four
+    // warps take columns 0-127 and 128-255, or units 0-63 and 64-127 of the
+    // gate and up halves.
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t tempty_leader = map_to_cta(tempty, 0);
+    const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+    uint32_t acc_phase = 0;
+    const int rt = q * 32 + lane;  // row of this CTA's 128
+    for (int tile = cid; tile < total; tile += ncl) {
+      const MxTile t = mx_tile(tile, n_wb, s_off, s_mt, G);
+      if (!__all_sync(0xffffffffu, mbar_wait(tfull, acc_phase, s_abort, status, limit_ns))) break;
+      acc_phase ^= 1u;
+      tc_fence_after();
+      uint32_t v[4][32];
+      __syncwarp();
+      if (kGateUp) {
+        tmem_ld_x32(tbase + half * 64, v[0]);
+        tmem_ld_x32(tbase + half * 64 + 32, v[1]);
+        tmem_ld_x32(tbase + 128 + half * 64, v[2]);
+        tmem_ld_x32(tbase + 128 + half * 64 + 32, v[3]);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld_x32(tbase + half * 128 + c * 32, v[c]);
+      }
+      tmem_ld_wait();
+      tc_fence_before();
+      mbar_arrive_cluster(tempty_leader);
+      const int in_group = t.m * 256 + (int)rank * 128 + rt;
+      const bool live = in_group < t.cnt;
+      const long long row = t.row0 + in_group;
+      if (kGateUp) {
+        if (live) {
+          uint32_t sbytes = 0;
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            const int unit0 = t.n * 128 + half * 64 + b * 32;
+            float h[32];
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              h[i] = silu_f32(__uint_as_float(v[b][i])) * __uint_as_float(v[2 + b][i]);
+              m = max(m, __float_as_uint(h[i]) & 0x7fffffffu);
+            }
+            if (unit0 < N) {
+              const uint32_t sb = mx_scale_byte(m);
+              const float inv = mx_inv_scale(sb);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) h[i] *= inv;
+              *reinterpret_cast<uint4*>(out.h + (size_t)row * (N / 2) + unit0 / 2) =
+                  make_uint4(mx_pack8(h), mx_pack8(h + 8), mx_pack8(h + 16), mx_pack8(h + 24));
+              sbytes |= sb << (8 * b);
+            }
+          }
+          // two of the four bytes of this row in the block's tile of scales
+          *reinterpret_cast<uint16_t*>(
+              out.h_scales + mx_scale_at((size_t)(2 * (s_mt[t.g] + t.m) + (int)rank), mx_stages(N), rt,
+                                         t.n * 4 + half * 2)) = (uint16_t)sbytes;
+        }
+      } else if (live) {
+        const float gs = out.gate ? out.gate[row] : 1.f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int n0 = t.n * 256 + half * 128 + c * 32;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float f[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = gs * __uint_as_float(v[c][8 * j + i]);
+            if (n0 + 8 * j < N) {
+              if (out.f32) {
+                float4* dst = reinterpret_cast<float4*>(static_cast<float*>(out.out) + (size_t)row * N + n0 + 8 * j);
+                dst[0] = make_float4(f[0], f[1], f[2], f[3]);
+                dst[1] = make_float4(f[4], f[5], f[6], f[7]);
+              } else {
+                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out.out) + (size_t)row * N + n0 + 8 * j) =
+                    make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                               pack_bf16x2(f[6], f[7]));
+              }
+            }
+          }
+        }
+      }
+    }
+  }
+
+  pdl_trigger();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // no CTA leaves while its peer may still touch its shared memory or TMEM
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, 512);
+  }
+}
+
+// Resident CTA pairs per GPU, queried once per device and kernel.
+int max_pairs(const void* kern, std::atomic<int>* cache) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  const int have = cache[dev].load(std::memory_order_acquire);
+  if (have > 0) return have;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2, 1, 1);
+  cfg.blockDim = dim3(kMxThreads, 1, 1);
+  cfg.dynamicSmemBytes = kMxSmem;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 2;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) return 0;
+  cache[dev].store(n, std::memory_order_release);
+  return n;
+}
+
+template <bool kGateUp>
+cudaError_t launch(const MxMaps& m, const int32_t* offsets, int G, int M, int N, int K, int group_tiles,
+                   const MxOut& out, int32_t* status, cudaStream_t stream) {
+  static std::atomic<int> cache[64];
+  auto kern = mx_gemm_kernel<kGateUp>;
+  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMxSmem);
+  if (err != cudaSuccess) return err;
+  const int pairs = max_pairs(reinterpret_cast<const void*>(kern), cache);
+  if (pairs <= 0) return cudaErrorInvalidConfiguration;
+  const long long n_wb = kGateUp ? (N + 127) / 128 : (N + 255) / 256;
+  const long long row_tiles = offsets ? (long long)M / 256 + G : (long long)G * ((M + 255) / 256);
+  const long long most = row_tiles * n_wb;
+  const int clusters = (int)(most < pairs ? most : pairs);
+  if (clusters <= 0) return cudaSuccess;
+  return launch_pdl(kern, dim3(2 * clusters), dim3(kMxThreads), kMxSmem, stream, m.a, m.sa, m.b0, m.b1, m.sb0, m.sb1,
+                    offsets, G, M, N, K, group_tiles, out, status, kWaitLimitNs);
+}
+
+}  // namespace
+
+cudaError_t launch_mx_product(const MxMaps& m, const int32_t* offsets, int G, int M, int N, int K, int group_tiles,
+                              const MxOut& out, int32_t* status, cudaStream_t stream) {
+  return launch<false>(m, offsets, G, M, N, K, group_tiles, out, status, stream);
+}
+
+cudaError_t launch_mx_gateup(const MxMaps& m, const int32_t* offsets, int G, int M, int N, int K, int group_tiles,
+                             const MxOut& out, int32_t* status, cudaStream_t stream) {
+  return launch<true>(m, offsets, G, M, N, K, group_tiles, out, status, stream);
+}
+
+}  // namespace moe

@@ -1,0 +1,75 @@
+// mx_internal.h — launchers of the MXFP4 kernels (host-side declarations).
+#pragma once
+
+#include "moe_internal.h"
+
+namespace moe {
+
+// Rows of 128-row scale tiles that one group of `rows` rows takes (a group
+// starts at a new pair of tiles).
+inline long long mx_group_tiles(long long rows) { return (rows + 255) / 256 * 2; }
+// Pieces of 256 columns (one pipeline stage of the product) of a row.
+inline int mx_stage_count(int cols) { return (cols + 255) / 256; }
+
+// Rows to MXFP4 and back. offsets == NULL: x is [n_rows / rows, rows, cols],
+// every group padded to group_tiles tile rows of scales; otherwise x is
+// [n_rows, cols] with G <= kMaxExperts groups at offsets[0..G]. tile_rows: tile
+// rows that the scales hold (nothing is written or read past them).
+cudaError_t launch_mx_quantize(moe_dtype dtype, const void* x, long long n_rows, int rows, int cols,
+                               const int32_t* offsets, int G, int group_tiles, size_t tile_rows, void* data,
+                               void* scales, cudaStream_t stream);
+cudaError_t launch_mx_dequantize(moe_dtype dtype, const void* data, const void* scales, long long n_rows, int rows,
+                                 int cols, const int32_t* offsets, int G, int group_tiles, size_t tile_rows, void* out,
+                                 cudaStream_t stream);
+
+// Tensor maps of one MXFP4 product: codes and scales of A, and of one or two
+// weights (the product repeats the first).
+struct MxMaps {
+  CUtensorMap a, sa, b0, b1, sb0, sb1;
+};
+
+// Where an MXFP4 product writes: out [M, N] fp32 or bf16, each row multiplied
+// by gate[row] (NULL: 1), or for gate/up the MXFP4 hidden rows.
+struct MxOut {
+  void* out;
+  int f32;
+  const float* gate;
+  uint8_t* h;
+  uint8_t* h_scales;
+};
+
+// out[r] = gate[r] * A[r] . B[g]^T for the rows r of each group g (offsets
+// NULL: G groups of M rows each; otherwise M rows in all). N: weight rows per
+// group, group_tiles: tile rows of scales per weight group.
+cudaError_t launch_mx_product(const MxMaps& m, const int32_t* offsets, int G, int M, int N, int K, int group_tiles,
+                              const MxOut& out, int32_t* status, cudaStream_t stream);
+// H[r] = MXFP4(SiLU(A[r] . B0[g]^T) * (A[r] . B1[g]^T)), N hidden units.
+cudaError_t launch_mx_gateup(const MxMaps& m, const int32_t* offsets, int G, int M, int N, int K, int group_tiles,
+                             const MxOut& out, int32_t* status, cudaStream_t stream);
+
+// Codes [rows, row_bytes] in boxes of 128 rows x 128 bytes (128-byte swizzle),
+// and scales as rows of 1024 bytes, one row a box. False on failure.
+bool make_tmap_mx_codes(CUtensorMap* map, const void* base, uint64_t rows, uint64_t row_bytes);
+bool make_tmap_mx_scales(CUtensorMap* map, const void* base, uint64_t rows);
+
+// The dispatch of given choices: per block of kRouterTokensTc tokens the
+// counts of every expert, the rank of every (token, slot) among the block's
+// assignments of its expert (slots of a token in order), and zeros in
+// blk_psum. A choice outside [0, E) sets MOE_DEV_INTERNAL and gets rank -1.
+// clear_status: the word is the call's own and is cleared first.
+cudaError_t launch_mx_count(const int32_t* topk_idx, int T, int E, int k, int32_t* lrank, int32_t* blk_cnt,
+                            float* blk_psum, int32_t* status, cudaStream_t stream);
+
+// Each token's row of x to MXFP4 once, written at the row of each of its
+// choices (base row of its block and expert plus its rank); also inv [T, k]
+// (-1 for a choice out of range) and the rows' gates.
+cudaError_t launch_mx_dispatch(moe_dtype dtype, const void* x, int T, int d, int E, int k, int rb,
+                               const int32_t* topk_idx, const int32_t* lrank, const int32_t* blk_base,
+                               const int32_t* offsets, const int32_t* mtile, const float* topk_gate, int32_t* inv,
+                               float* rgate, void* data, void* scales, int32_t* status, cudaStream_t stream);
+
+// out[t] = sum over t's choices of the rows Y[inv[t, j]] (bf16, gated already).
+cudaError_t launch_mx_combine(const void* y, const int32_t* inv, int T, int d, int k, void* out, int32_t* status,
+                              cudaStream_t stream);
+
+}  // namespace moe

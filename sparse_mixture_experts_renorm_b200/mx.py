@@ -1,0 +1,273 @@
+"""MXFP4 (microscaled 4-bit) matrices and the layer with its experts in them:
+``mx_quantize`` / ``mx_dequantize``, ``mx_matmul``, ``mx_experts`` and
+``moe_forward_mx`` (``moe_mx_*`` in include/moe.h, which has the formulas)."""
+from __future__ import annotations
+
+import ctypes
+from dataclasses import dataclass
+
+import torch
+
+from . import _binding as B
+from ._call import check, cuda, device_status, dtype_code, need, on, ptr
+
+_BYTE = torch.uint8
+
+
+@dataclass
+class MXTensor:
+    """An MXFP4 matrix or stack of matrices: ``data`` [rows, cols / 2] or
+    [groups, rows, cols / 2] uint8 (two E2M1 codes a byte, the even column in
+    the low half) and ``scales``, the E8M0 bytes in the library's tiles
+    (include/moe.h has the layout; ``mx_scale_bytes`` of them)."""
+    data: torch.Tensor
+    scales: torch.Tensor
+
+    @property
+    def shape(self):
+        return torch.Size((*self.data.shape[:-1], 2 * self.data.shape[-1]))
+
+    @property
+    def device(self):
+        return self.data.device
+
+
+def mx_scale_bytes(groups: int, rows: int, cols: int, ragged: bool = False) -> int:
+    """Bytes of scales of ``groups`` groups of ``rows`` rows each, or (ragged)
+    of ``rows`` rows in ``groups`` groups of any lengths."""
+    lib = B.load_library()
+    n = lib.moe_mx_scale_bytes(groups, rows, cols, int(ragged))
+    if n == 0:
+        raise B.MoEError(B.MOE_ERR_INVALID_ARG, B.last_error_detail(lib))
+    return int(n)
+
+
+def _offsets(offsets, dev):
+    """(pointer, groups) of ragged groups; offsets [groups + 1] int32."""
+    if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.numel() < 2:
+        raise ValueError("offsets must be a one-dimensional int32 tensor of groups + 1 row numbers")
+    need("offsets", offsets, torch.int32, None, dev)
+    return offsets.data_ptr(), offsets.numel() - 1
+
+
+def _check_mx(name, q, dev):
+    if not isinstance(q, MXTensor):
+        raise TypeError(f"{name} must be an MXTensor")
+    if q.data.dim() not in (2, 3):
+        raise ValueError(f"{name}.data must be [rows, cols / 2] or [groups, rows, cols / 2]")
+    need(f"{name}.data", q.data, _BYTE, None, dev)
+    need(f"{name}.scales", q.scales, _BYTE, None, dev)
+
+
+def mx_quantize(x, offsets=None, *, stream=None) -> MXTensor:
+    """``x`` ([rows, cols] or [groups, rows, cols], bf16 or fp32, contiguous,
+    cols % 32 == 0) in MXFP4. With ``offsets`` ([groups + 1] int32 on the
+    device, ``x`` [rows, cols]) group g is rows offsets[g] .. offsets[g + 1] - 1;
+    rows of no group get no codes."""
+    dev = cuda("x", x)
+    if x.dim() not in (2, 3) or (offsets is not None and x.dim() != 2):
+        raise ValueError("x must be [rows, cols], or [groups, rows, cols] without offsets")
+    dt = dtype_code(x.dtype)
+    need("x", x, x.dtype, None, dev)
+    lib = B.load_library()
+    rows, cols = x.shape[-2], x.shape[-1]
+    off, groups = _offsets(offsets, dev) if offsets is not None else (None, x.shape[0] if x.dim() == 3 else 1)
+    with on(dev, stream) as s:
+        n = mx_scale_bytes(groups, rows, cols, offsets is not None)
+        data = torch.empty((*x.shape[:-1], cols // 2), dtype=_BYTE, device=dev)
+        scales = torch.empty((n,), dtype=_BYTE, device=dev)
+        check(lib.moe_mx_quantize(ptr(x), off, groups, rows, cols, dt, ptr(data), ptr(scales), n, s), lib)
+    return MXTensor(data, scales)
+
+
+def mx_dequantize(q: MXTensor, dtype=torch.bfloat16, offsets=None, *, out=None, stream=None) -> torch.Tensor:
+    """The values of ``q`` in ``dtype`` (bf16 or fp32: exact in both). With
+    ``offsets`` as given to ``mx_quantize``; rows of no group are left as they
+    are in ``out`` (unset in a new one)."""
+    if not isinstance(q, MXTensor):
+        raise TypeError("q must be an MXTensor")
+    dev = cuda("q.data", q.data)
+    _check_mx("q", q, dev)
+    dt = dtype_code(dtype)
+    if offsets is not None and q.data.dim() != 2:
+        raise ValueError("a matrix with offsets is [rows, cols]")
+    lib = B.load_library()
+    rows, cols = q.shape[-2], q.shape[-1]
+    off, groups = _offsets(offsets, dev) if offsets is not None else (None, q.shape[0] if q.data.dim() == 3 else 1)
+    with on(dev, stream) as s:
+        if out is None:
+            out = torch.empty(q.shape, dtype=dtype, device=dev)
+        need("out", out, dtype, q.shape, dev)
+        check(lib.moe_mx_dequantize(ptr(q.data), ptr(q.scales), q.scales.numel(), off, groups, rows, cols, dt,
+                                    ptr(out), s), lib)
+    return out
+
+
+def mx_matmul(a: MXTensor, b: MXTensor, offsets=None, *, out_dtype=torch.bfloat16, out=None, status=None,
+              stream=None) -> torch.Tensor:
+    """out[r] = a[r] @ b[g].T for the rows r of every group g: ``a`` [M, K] with
+    ``offsets`` [groups + 1] (and quantised with them), or [M, K] / [groups, M,
+    K] without; ``b`` [N, K] or [groups, N, K], N % 8 == 0. The result is [M, N]
+    or [groups, M, N] in ``out_dtype`` (bf16 or fp32); rows of no group are left
+    as they are. ``status``: [1] int32, MOE_DEV_* bits are OR-ed in (default:
+    ``device_status`` of the device)."""
+    if not isinstance(a, MXTensor):
+        raise TypeError("a must be an MXTensor")
+    dev = cuda("a.data", a.data)
+    _check_mx("a", a, dev)
+    _check_mx("b", b, dev)
+    dt = dtype_code(out_dtype)
+    groups = b.data.shape[0] if b.data.dim() == 3 else 1
+    N, K = b.shape[-2], b.shape[-1]
+    M = a.shape[-2]
+    off = None
+    if offsets is not None:
+        off, n = _offsets(offsets, dev)
+        if a.data.dim() != 2 or n != groups:
+            raise ValueError(f"with offsets a is [M, K] and there are as many groups as in b ({groups})")
+    elif (a.data.shape[0] if a.data.dim() == 3 else 1) != groups:
+        raise ValueError("without offsets a and b have the same number of groups")
+    if a.shape[-1] != K:
+        raise ValueError(f"a has {a.shape[-1]} columns and b {K}")
+    lib = B.load_library()
+    for name, q, g, rows, ragged in (("a", a, groups, M, off is not None), ("b", b, groups, N, False)):
+        n = mx_scale_bytes(g, rows, K, ragged)
+        if q.scales.numel() < n:
+            raise ValueError(f"{name}.scales holds {q.scales.numel()} bytes, {n} are needed")
+    if status is None:
+        status = device_status(dev)
+    need("status", status, torch.int32, (1,), dev)
+    shape = (*a.data.shape[:-1], N)
+    with on(dev, stream) as s:
+        if out is None:
+            out = torch.empty(shape, dtype=out_dtype, device=dev)
+        need("out", out, out_dtype, shape, dev)
+        check(lib.moe_mx_matmul(ptr(a.data), ptr(a.scales), ptr(b.data), ptr(b.scales), off, groups, M, N, K, dt,
+                                ptr(out), ptr(status), s), lib)
+    return out
+
+
+@dataclass
+class MXOutputs:
+    out: torch.Tensor  # [T, d] bf16
+    counts: torch.Tensor  # [E] int32
+    status: torch.Tensor  # [1] int32, MOE_DEV_* bits of this call
+    workspace: torch.Tensor  # uint8
+    topk_idx: torch.Tensor | None = None  # [T, k] int32 (moe_forward_mx)
+    topk_gate: torch.Tensor | None = None  # [T, k] fp32 (moe_forward_mx)
+    aux: torch.Tensor | None = None  # [1] fp32 (moe_forward_mx)
+
+
+def mx_workspace_size(T: int, d: int, E: int, k: int, I: int) -> int:
+    """Bytes of scratch of ``mx_experts`` and ``moe_forward_mx``."""
+    lib = B.load_library()
+    n = lib.moe_mx_workspace_size(T, d, E, k, I)
+    if n == 0:
+        raise B.MoEError(B.MOE_ERR_INVALID_ARG, B.last_error_detail(lib))
+    return int(n)
+
+
+def _weights(w_gate, w_up, w_down, dev, d):
+    for name, q in (("w_gate", w_gate), ("w_up", w_up), ("w_down", w_down)):
+        _check_mx(name, q, dev)
+        if q.data.dim() != 3:
+            raise ValueError(f"{name} must be [E, rows, cols]")
+    E, I, _ = w_gate.shape
+    for name, q, shape in (("w_gate", w_gate, (E, I, d)), ("w_up", w_up, (E, I, d)), ("w_down", w_down, (E, d, I))):
+        if tuple(q.shape) != shape:
+            raise ValueError(f"{name} must have the shape {shape} (got {tuple(q.shape)})")
+        n = mx_scale_bytes(*shape)
+        if q.scales.numel() < n:
+            raise ValueError(f"{name}.scales holds {q.scales.numel()} bytes, {n} are needed")
+    w = B.moe_mx_weights()
+    w.struct_bytes = ctypes.sizeof(B.moe_mx_weights)
+    w.gate, w.gate_scales = w_gate.data.data_ptr(), w_gate.scales.data_ptr()
+    w.up, w.up_scales = w_up.data.data_ptr(), w_up.scales.data_ptr()
+    w.down, w.down_scales = w_down.data.data_ptr(), w_down.scales.data_ptr()
+    return w, E, I
+
+
+def _buffers(x, T, d, E, k, I, out, counts, workspace, status):
+    dev = x.device
+    if out is None:
+        out = torch.empty((T, d), dtype=torch.bfloat16, device=dev)
+    need("out", out, torch.bfloat16, (T, d), dev)
+    if counts is None:
+        counts = torch.empty((E,), dtype=torch.int32, device=dev)
+    need("counts", counts, torch.int32, (E,), dev)
+    size = mx_workspace_size(T, d, E, k, I)
+    if workspace is None:
+        workspace = torch.empty((size,), dtype=_BYTE, device=dev)
+    need("workspace", workspace, _BYTE, None, dev)
+    if status is not None:
+        need("status", status, torch.int32, (1,), dev)
+    return out, counts, workspace
+
+
+def _status_of(status, workspace):
+    """The call's own status word is the workspace's first four bytes."""
+    return workspace[:4].view(torch.int32) if status is None else status
+
+
+def _rows(x):
+    dev = cuda("x", x)
+    if x.dim() != 2:
+        raise ValueError("x must be [T, d]")
+    dt = dtype_code(x.dtype)
+    need("x", x, x.dtype, None, dev)
+    return dev, dt
+
+
+def mx_experts(x, topk_idx, topk_gate, w_gate: MXTensor, w_up: MXTensor, w_down: MXTensor, *, out=None, counts=None,
+               workspace=None, status=None, stream=None) -> MXOutputs:
+    """The layer's experts in MXFP4 for given choices: ``x`` [T, d] (bf16 or
+    fp32), ``topk_idx`` [T, k] int32, ``topk_gate`` [T, k] fp32, weights
+    [E, I, d], [E, I, d] and [E, d, I]. out[t] = sum_j gate[t, j] y of expert
+    idx[t, j], bf16. Without ``status`` the call's word is the workspace's
+    first four bytes (cleared by the call)."""
+    dev, dt = _rows(x)
+    T, d = x.shape
+    w, E, I = _weights(w_gate, w_up, w_down, dev, d)
+    if topk_idx.dim() != 2:
+        raise ValueError("topk_idx must be [T, k]")
+    k = topk_idx.shape[1]
+    need("topk_idx", topk_idx, torch.int32, (T, k), dev)
+    need("topk_gate", topk_gate, torch.float32, (T, k), dev)
+    lib = B.load_library()
+    with on(dev, stream) as s:
+        out, counts, workspace = _buffers(x, T, d, E, k, I, out, counts, workspace, status)
+        check(lib.moe_mx_experts(ptr(x), ptr(topk_idx), ptr(topk_gate), ctypes.byref(w), T, d, E, k, I, dt, ptr(out),
+                                 ptr(counts), ptr(workspace), workspace.numel(), ptr(status), s), lib)
+        status = _status_of(status, workspace)
+    return MXOutputs(out, counts, status, workspace)
+
+
+def moe_forward_mx(x, w_router, b_router, w_gate: MXTensor, w_up: MXTensor, w_down: MXTensor, k: int, renorm: bool, *,
+                   out=None, topk_idx=None, topk_gate=None, counts=None, aux=None, workspace=None, status=None,
+                   stream=None) -> MXOutputs:
+    """``moe_forward`` with the experts in MXFP4: the router runs on ``x`` and
+    ``w_router`` [E, d] as they are (one dtype, bf16 or fp32; ``b_router`` [E]
+    fp32 or None), then ``mx_experts`` on its choices."""
+    dev, dt = _rows(x)
+    T, d = x.shape
+    w, E, I = _weights(w_gate, w_up, w_down, dev, d)
+    need("w_router", w_router, x.dtype, (E, d), dev)
+    if b_router is not None:
+        need("b_router", b_router, torch.float32, (E,), dev)
+    lib = B.load_library()
+    with on(dev, stream) as s:
+        out, counts, workspace = _buffers(x, T, d, E, k, I, out, counts, workspace, status)
+        if topk_idx is None:
+            topk_idx = torch.empty((T, k), dtype=torch.int32, device=dev)
+        if topk_gate is None:
+            topk_gate = torch.empty((T, k), dtype=torch.float32, device=dev)
+        if aux is None:
+            aux = torch.empty((1,), dtype=torch.float32, device=dev)
+        need("topk_idx", topk_idx, torch.int32, (T, k), dev)
+        need("topk_gate", topk_gate, torch.float32, (T, k), dev)
+        need("aux", aux, torch.float32, (1,), dev)
+        check(lib.moe_mx_forward(ptr(x), ptr(w_router), ptr(b_router), ctypes.byref(w), T, d, E, k, I,
+                                 int(bool(renorm)), dt, ptr(out), ptr(topk_idx), ptr(topk_gate), ptr(counts),
+                                 ptr(aux), ptr(workspace), workspace.numel(), ptr(status), s), lib)
+        status = _status_of(status, workspace)
+    return MXOutputs(out, counts, status, workspace, topk_idx, topk_gate, aux)
