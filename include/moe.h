@@ -360,6 +360,28 @@ void* moe_pipeline_stream(const moe_pipeline* p, int which);
 moe_status moe_pipeline_destroy(moe_pipeline* p);
 
 /*
+ * moe_forward_few — the layer for at most MOE_FEW_TOKENS tokens (the next
+ * tokens of a few sequences) in two kernels: the routing and the gate/up
+ * products in one, the down products and the sum over a token's experts in
+ * the other. Arguments as for moe_forward, but
+ *   out         [T, d] in `dtype`: a token's expert outputs are added in fp32
+ *               in slot order and rounded once
+ *   counts, aux may be NULL: they are then not computed
+ *   status_dev  device int32 [1], required (MOE_DEV_* bits are OR-ed in)
+ *   workspace   moe_few_workspace_size() bytes, 256-byte aligned, any contents;
+ *               calls that overlap on the GPU need one each
+ * MOE_BF16: d % 8 == 0 and I % 8 == 0; MOE_F32: d % 4 == 0 and I % 4 == 0.
+ * Experts rank by their logits (as their exact probabilities do). Results are
+ * bit-identical from run to run.
+ */
+#define MOE_FEW_TOKENS 16
+size_t moe_few_workspace_size(int T, int d, int E, int k, int I, moe_dtype dtype);
+moe_status moe_forward_few(const void* x, const void* w_router, const float* b_router, const void* w_gate,
+                           const void* w_up, const void* w_down, int T, int d, int E, int k, int I, int renorm,
+                           moe_dtype dtype, void* out, int32_t* topk_idx, float* topk_gate, int32_t* counts,
+                           float* aux, void* workspace, size_t workspace_bytes, int32_t* status_dev, void* stream);
+
+/*
  * MXFP4 (OCP microscaling formats, "MX"): a matrix [rows, cols] as
  *   codes   uint8 [rows, cols / 2]: E2M1 elements (0, 0.5, 1, 1.5, 2, 3, 4, 6
  *           and their negatives), element 2i in the low, 2i + 1 in the high

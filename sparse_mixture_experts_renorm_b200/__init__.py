@@ -17,12 +17,14 @@ import torch
 from . import _binding as B
 from ._binding import MoEError, load_library
 from ._call import device_status
+from .few import FewOutputs, few_workspace_size, moe_forward_few
 from .mx import (MXOutputs, MXTensor, moe_forward_mx, mx_dequantize, mx_experts, mx_matmul, mx_quantize,
                  mx_scale_bytes, mx_workspace_size)
 
 __all__ = ["MoEError", "MoEOptions", "MoEOutputs", "MoELayer", "HostPipeline", "moe_forward", "workspace_size",
            "get_permutation", "launch_plan", "load_library", "MXTensor", "MXOutputs", "mx_quantize", "mx_dequantize",
-           "mx_matmul", "mx_experts", "moe_forward_mx", "mx_scale_bytes", "mx_workspace_size", "device_status"]
+           "mx_matmul", "mx_experts", "moe_forward_mx", "mx_scale_bytes", "mx_workspace_size", "device_status",
+           "FewOutputs", "few_workspace_size", "moe_forward_few"]
 
 
 def _dtype_code(t: torch.dtype) -> int:

@@ -30,10 +30,11 @@ EXPORTED = ("moe_workspace_size", "moe_forward", "moe_forward_events", "moe_kern
             "moe_forward_ex", "moe_launch_plan", "moe_pipeline_create", "moe_pipeline_submit",
             "moe_pipeline_synchronize", "moe_pipeline_stream", "moe_pipeline_destroy", "moe_mx_scale_bytes",
             "moe_mx_quantize", "moe_mx_dequantize", "moe_mx_matmul", "moe_mx_workspace_size", "moe_mx_experts",
-            "moe_mx_forward")
+            "moe_mx_forward", "moe_few_workspace_size", "moe_forward_few")
 MOE_NORM_NONE, MOE_NORM_RMS, MOE_NORM_RMS_EPS_OUTSIDE = 0, 1, 2
 MOE_MAX_SHARED = 8
 MOE_NOALLOC_SCRATCH_BYTES = 16 << 20
+MOE_FEW_TOKENS = 16
 MOE_NUM_KERNELS = 6
 MOE_PLAN_FUSED_COMBINE, MOE_PLAN_FUSED_GEMMS, MOE_PLAN_ROUTER_WEIGHT_SPLIT, MOE_PLAN_FUSED_SCAN = 1, 2, 4, 8
 MOE_PLAN_PERMUTE_SCAN = 16
@@ -171,6 +172,10 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.moe_mx_experts.restype = I32
     lib.moe_mx_forward.argtypes = [P, P, P, MXW, I32, I32, I32, I32, I32, I32, I32, P, P, P, P, P, P, SZ, P, P]
     lib.moe_mx_forward.restype = I32
+    lib.moe_few_workspace_size.argtypes = [I32, I32, I32, I32, I32, I32]
+    lib.moe_few_workspace_size.restype = SZ
+    lib.moe_forward_few.argtypes = lib.moe_forward.argtypes
+    lib.moe_forward_few.restype = I32
     lib.moe_last_error_detail.argtypes = [ctypes.c_char_p, SZ]
     lib.moe_last_error_detail.restype = SZ
     if path is None:

@@ -1,0 +1,42 @@
+// few_internal.h — the layer for a few tokens: limits, workspace and launcher
+// (host-side declarations).
+#pragma once
+
+#include "moe_internal.h"
+
+namespace moe {
+
+constexpr int kFewTokens = MOE_FEW_TOKENS;  // two n8 tiles of an mma.sync step
+constexpr int kFewMaxSplit = 8;   // parts of a down product's columns
+
+// Byte offsets inside the workspace.
+struct FewWorkspace {
+  size_t done;   // int32 [blocks of 16 output columns] finished parts
+  size_t h;      // dtype [T*k, I] hidden rows in expert order
+  size_t y;      // fp32  [split, T*k, d] gated expert outputs
+  size_t total;
+  int split;     // parts that y has room for
+};
+
+struct FewArgs {
+  const void *x, *wr, *wg, *wu, *wd;
+  const float* br;
+  int T, d, E, k, I, renorm;
+  void* out;
+  int32_t* idx;
+  float* gate;
+  int32_t* counts;  // NULL: not wanted
+  float* aux;       // NULL: not wanted
+  int32_t* done;
+  void* h;
+  float* y;
+  int split;        // parts that y has room for
+  int stages;       // ring stages, set by the launcher
+  int32_t* status;
+  uint64_t limit_ns;
+};
+
+FewWorkspace few_layout(int T, int d, int k, int I, moe_dtype dtype);
+cudaError_t launch_few(moe_dtype dtype, FewArgs a, cudaStream_t stream);
+
+}  // namespace moe

@@ -1,0 +1,83 @@
+"""The layer for a few tokens in two kernels: ``moe_forward_few`` (include/moe.h
+has the definition)."""
+from __future__ import annotations
+
+from dataclasses import dataclass
+
+import torch
+
+from . import _binding as B
+from ._call import check, cuda, device_status, dtype_code, need, on, ptr
+
+
+@dataclass
+class FewOutputs:
+    out: torch.Tensor  # [T, d] in x's dtype
+    topk_idx: torch.Tensor  # [T, k] int32
+    topk_gate: torch.Tensor  # [T, k] fp32
+    status: torch.Tensor  # [1] int32, MOE_DEV_* bits are OR-ed in
+    counts: torch.Tensor | None = None  # [E] int32, when given
+    aux: torch.Tensor | None = None  # [1] fp32, when given
+
+
+def few_workspace_size(T: int, d: int, E: int, k: int, I: int, dtype: torch.dtype) -> int:
+    """Bytes of scratch of ``moe_forward_few``."""
+    lib = B.load_library()
+    n = lib.moe_few_workspace_size(T, d, E, k, I, dtype_code(dtype))
+    if n == 0:
+        raise B.MoEError(B.MOE_ERR_INVALID_ARG, B.last_error_detail(lib))
+    return int(n)
+
+
+def moe_forward_few(x, w_router, b_router, w_gate, w_up, w_down, k: int, renorm: bool, *, out=None, topk_idx=None,
+                    topk_gate=None, counts=None, aux=None, workspace=None, status=None, stream=None) -> FewOutputs:
+    """``moe_forward`` for ``x`` of at most 16 tokens ([T, d], bf16 or fp32), in
+    two kernels, with the output in x's dtype. ``counts`` ([E] int32) and
+    ``aux`` ([1] fp32) are filled when given. ``workspace``: uint8,
+    ``few_workspace_size`` bytes, one for each call that may run at the same
+    time (default: a new one). ``status``: [1] int32 (default:
+    ``device_status`` of the device)."""
+    dev = cuda("x", x)
+    dt = x.dtype
+    code = dtype_code(dt)
+    if x.dim() != 2 or w_gate.dim() != 3:
+        raise ValueError("x must be [T, d] and w_gate [E, I, d]")
+    T, d = x.shape
+    E, I, _ = w_gate.shape
+    need("x", x, dt, (T, d), dev)
+    need("w_router", w_router, dt, (E, d), dev)
+    need("w_gate", w_gate, dt, (E, I, d), dev)
+    need("w_up", w_up, dt, (E, I, d), dev)
+    need("w_down", w_down, dt, (E, d, I), dev)
+    if b_router is not None:
+        need("b_router", b_router, torch.float32, (E,), dev)
+    if counts is not None:
+        need("counts", counts, torch.int32, (E,), dev)
+    if aux is not None:
+        need("aux", aux, torch.float32, (1,), dev)
+    if status is None:
+        status = device_status(dev)
+    else:
+        need("status", status, torch.int32, (1,), dev)
+    lib = B.load_library()
+    with on(dev, stream) as s:
+        if workspace is None:
+            workspace = torch.empty((few_workspace_size(T, d, E, k, I, dt),), dtype=torch.uint8, device=dev)
+        else:
+            need("workspace", workspace, torch.uint8, None, dev)
+        if out is None:
+            out = torch.empty((T, d), dtype=dt, device=dev)
+        else:
+            need("out", out, dt, (T, d), dev)
+        if topk_idx is None:
+            topk_idx = torch.empty((T, k), dtype=torch.int32, device=dev)
+        else:
+            need("topk_idx", topk_idx, torch.int32, (T, k), dev)
+        if topk_gate is None:
+            topk_gate = torch.empty((T, k), dtype=torch.float32, device=dev)
+        else:
+            need("topk_gate", topk_gate, torch.float32, (T, k), dev)
+        check(lib.moe_forward_few(ptr(x), ptr(w_router), ptr(b_router), ptr(w_gate), ptr(w_up), ptr(w_down), T, d, E,
+                                  k, I, int(bool(renorm)), code, ptr(out), ptr(topk_idx), ptr(topk_gate), ptr(counts),
+                                  ptr(aux), ptr(workspace), workspace.numel(), ptr(status), s), lib)
+    return FewOutputs(out, topk_idx, topk_gate, status, counts, aux)
