@@ -37,9 +37,13 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kMathWarps = 8;
 constexpr int kMath = 32 * kMathWarps;
 constexpr int kRows = 16;                // weight rows of a stage
-constexpr int kChunk = 1024;             // bytes of a row in a stage
-constexpr int kRowStride = kChunk + 64;  // two rows of a quarter-warp's load fall on different banks
-constexpr int kMaxStages = 12;
+constexpr int kBox = 512;                // bytes of a row in one tile load
+constexpr int kBoxes = 4;                // tile loads side by side in a stage
+constexpr int kChunk = kBox * kBoxes;    // bytes of a row in a stage
+constexpr int kWeightBytes = kRows * kChunk;
+constexpr int kTokPitch = kFewTokPitch;  // bytes between token rows: two rows of a quarter-warp's load on different banks
+static_assert(kTokPitch == kChunk + 64, "pitch");
+constexpr int kMaxStages = 8;
 constexpr int kMaxRows = kFewTokens * kMaxTopK;
 constexpr int kCluster = 4;              // CTAs that share one routing
 constexpr int kPassE = 64;               // experts whose logits a warp holds at a time
@@ -47,6 +51,7 @@ constexpr int kSmemTotal = 227 * 1024;
 
 struct Plan {
   int n_act;                        // experts with tokens
+  int most;                         // tokens of the one with most
   int expert[kMaxRows];             // ascending
   int base[kMaxRows + 1];           // first row of each
   int tj[kMaxRows];                 // t * k + j of a row
@@ -66,25 +71,42 @@ struct Ctrl {
   Plan plan;
 };
 
+// kParts: partial sums of an item (bf16: every warp has its own columns; fp32:
+// two halves of the columns, four groups of rows). kHid: rows that a hidden
+// row is stored as. bf16 keeps it in two terms, hi + lo, whose sum is off by
+// 2^-17: rounded to one, it would double the error that the output's own
+// rounding makes, and the second term costs only shared memory and issue slots
+// (both are columns of the same mma.sync while an expert has few tokens).
 template <typename X>
 struct Traits;
 template <>
 struct Traits<__nv_bfloat16> {
-  static constexpr int kParts = kMathWarps;  // partial sums of an item: every warp has its own columns
+  static constexpr int kParts = kMathWarps, kHid = 2;
 };
 template <>
 struct Traits<float> {
-  static constexpr int kParts = 2;  // two halves of the columns, four groups of rows
+  static constexpr int kParts = 2, kHid = 1;
 };
 constexpr int kRedLd = kFewTokens + 1;
 template <typename X>
 constexpr int red_floats() { return Traits<X>::kParts * kRows * kRedLd; }
 template <typename X>
-constexpr int fixed_bytes() { return (int)((sizeof(Ctrl) + 15) / 16 * 16 + 2 * red_floats<X>() * 4 + 16); }
+constexpr int fixed_bytes() { return (int)((sizeof(Ctrl) + 127) / 128 * 128 + 2 * red_floats<X>() * 4); }
 
-template <typename X>
-__host__ __device__ constexpr int slot_rows(int T) {
-  return kRows + (sizeof(X) == 4 ? (T + 3) / 4 * 4 : T);  // fp32 multiplies four token rows at a time
+// The ring's shape follows from the most tokens that an expert got.
+struct Ring {
+  uint8_t* base;
+  int slot, stages;
+};
+template <typename X, bool kUp>
+__device__ __forceinline__ Ring ring_of(uint8_t* base, const Plan& p) {
+  int rows = kUp ? p.most : p.most * Traits<X>::kHid;
+  if (sizeof(X) == 4) rows = (rows + 3) & ~3;  // fp32 multiplies four token rows at a time
+  Ring r;
+  r.base = base;
+  r.slot = (kWeightBytes + rows * kTokPitch + 127) & ~127;
+  r.stages = min(kMaxStages, (kSmemTotal - fixed_bytes<X>()) / r.slot);
+  return r;
 }
 
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -156,7 +178,7 @@ __device__ void make_plan(Plan& p, const int* idx, const float* gate, int T, int
   __syncthreads();
   if (threadIdx.x < 32) {
     const int lane = threadIdx.x;
-    int act = 0, rows = 0;
+    int act = 0, rows = 0, most = 0;
     for (int e0 = 0; e0 < E; e0 += 32) {
       const int e = e0 + lane;
       const int n = e < E ? __popc(p.mask[e]) : 0;
@@ -173,11 +195,13 @@ __device__ void make_plan(Plan& p, const int* idx, const float* gate, int T, int
         p.base[s] = rows + incl - n;
         p.slot[e] = s;
       }
+      most = max(most, (int)__reduce_max_sync(0xffffffffu, (unsigned)n));
       act += __popc(live);
       rows += __shfl_sync(0xffffffffu, incl, 31);
     }
     if (lane == 0) {
       p.n_act = act;
+      p.most = most;
       p.base[act] = rows;
     }
   }
@@ -423,8 +447,6 @@ struct Work {
   }
 };
 
-__device__ __forceinline__ int chunk_bytes(int c, int row_bytes) { return min(kChunk, row_bytes - c * kChunk); }
-
 // Ring position.
 struct Pos {
   int stage = 0;
@@ -434,112 +456,167 @@ struct Pos {
   }
 };
 
-// The two producers (kTokens: the token rows, else the weight rows). Lane l
-// copies row l of the stage.
-template <typename X, bool kUp, bool kTokens>
-__device__ void produce(const FewArgs& a, Ctrl& c, uint8_t* ring, int slot_bytes) {
+// Where an expert's hidden rows are: chunk after chunk of kChunk bytes, in each
+// all its rows (kHid of them for every token) kTokPitch bytes apart, so that a
+// stage's part is one contiguous copy.
+template <typename X>
+__device__ __forceinline__ size_t hidden_at(int first, int n, int chunks, int chunk, int row) {
+  constexpr int kHid = Traits<X>::kHid;
+  return (((size_t)first * chunks + (size_t)n * chunk) * kHid + row) * kTokPitch;
+}
+
+// The weights' producer: one lane. Rows past the last block's are read from
+// the next expert, or as zeros, and go into sums that nobody takes.
+template <typename X, bool kUp>
+__device__ bool produce_weights(const FewMaps& maps, const FewArgs& a, Ctrl& c, const Ring& ring, Pos& pos, int& issued) {
+  const Work<X, kUp> work(a, c.plan);
+  const int row_bytes = (kUp ? a.d : a.I) * (int)sizeof(X);
+  for (int i = blockIdx.x; i < work.total; i += gridDim.x) {
+    const Item w = work.item(i, c.plan);
+    const int e = c.plan.expert[w.s];
+    const int row = kUp ? e * a.I + w.blk * 8 : e * a.d + w.blk * kRows;
+    for (int ch = w.c0; ch < w.c1; ++ch) {
+      if (!mbar_wait(&c.empty[pos.stage], pos.phase ^ 1u, &c.abort, a.status, a.limit_ns)) return false;
+      uint8_t* dst = ring.base + (size_t)pos.stage * ring.slot;
+      const int boxes = min(kBoxes, (row_bytes - ch * kChunk + kBox - 1) / kBox);
+      mbar_arrive_expect_tx(&c.full[pos.stage], (uint32_t)(boxes * kRows * kBox));
+      for (int b = 0; b < boxes; ++b) {
+        const int col = (ch * kChunk + b * kBox) / (int)sizeof(X);
+        uint8_t* to = dst + b * kRows * kBox;
+        if (kUp) {  // rows 0..7: gate rows of 8 hidden units, 8..15: their up rows
+          tma_load_2d(to, &maps.wg, &c.full[pos.stage], col, row);
+          tma_load_2d(to + 8 * kBox, &maps.wu, &c.full[pos.stage], col, row);
+        } else {
+          tma_load_2d(to, &maps.wd, &c.full[pos.stage], col, row);
+        }
+      }
+      ++issued;
+      pos.next(ring.stages);
+    }
+  }
+  return true;
+}
+
+// The token rows' producer: one warp, lane l copies row l of x, or lane 0 all
+// hidden rows.
+template <typename X, bool kUp>
+__device__ bool produce_tokens(const FewArgs& a, Ctrl& c, const Ring& ring, Pos& pos, int& issued) {
   const int lane = threadIdx.x & 31;
   const Work<X, kUp> work(a, c.plan);
-  const int K = kUp ? a.d : a.I;
-  const int row_bytes = K * (int)sizeof(X);
-  Pos pos;
-  int issued = 0;
-  bool ok = true;
-  for (int i = blockIdx.x; ok && i < work.total; i += gridDim.x) {
+  const int row_bytes = (kUp ? a.d : a.I) * (int)sizeof(X);
+  for (int i = blockIdx.x; i < work.total; i += gridDim.x) {
     const Item w = work.item(i, c.plan);
-    const X* src = nullptr;  // this lane's row
-    int rows;
-    if (kTokens) {
-      rows = w.n;
-      if (lane < rows)
-        src = kUp ? static_cast<const X*>(a.x) + (size_t)(c.plan.tj[w.first + lane] / a.k) * a.d
-                  : static_cast<const X*>(a.h) + (size_t)(w.first + lane) * a.I;
-    } else {
-      const size_t e = (size_t)c.plan.expert[w.s];
-      if (kUp) {  // rows 0..7: gate rows of 8 hidden units, 8..15: their up rows
-        const int unit = w.blk * 8 + (lane & 7);
-        const int live = min(8, a.I - w.blk * 8);
-        rows = 2 * live;
-        if (lane < kRows && (lane & 7) < live)
-          src = static_cast<const X*>(lane < 8 ? a.wg : a.wu) + (e * a.I + unit) * (size_t)a.d;
-      } else {
-        rows = min(kRows, a.d - w.blk * kRows);
-        if (lane < rows) src = static_cast<const X*>(a.wd) + (e * a.d + w.blk * kRows + lane) * (size_t)a.I;
-      }
-    }
+    const uint8_t* src = nullptr;
+    if (kUp && lane < w.n)
+      src = static_cast<const uint8_t*>(a.x) + (size_t)(c.plan.tj[w.first + lane] / a.k) * row_bytes;
     for (int ch = w.c0; ch < w.c1; ++ch) {
+      const uint32_t bytes = kUp ? (uint32_t)min(kChunk, row_bytes - ch * kChunk)
+                                 : (uint32_t)(w.n * Traits<X>::kHid * kTokPitch);
       bool free = true;
       if (lane == 0) {
         free = mbar_wait(&c.empty[pos.stage], pos.phase ^ 1u, &c.abort, a.status, a.limit_ns);
-        if (free) mbar_arrive_expect_tx(&c.full[pos.stage], (uint32_t)(rows * chunk_bytes(ch, row_bytes)));
+        if (free) mbar_arrive_expect_tx(&c.full[pos.stage], kUp ? w.n * bytes : bytes);
       }
-      if (!__shfl_sync(0xffffffffu, (int)free, 0)) {
-        ok = false;
-        break;
-      }
-      if (src)
-        bulk_load(ring + (size_t)pos.stage * slot_bytes + (lane + (kTokens ? kRows : 0)) * kRowStride,
-                  reinterpret_cast<const uint8_t*>(src) + (size_t)ch * kChunk, (uint32_t)chunk_bytes(ch, row_bytes),
+      if (!__shfl_sync(0xffffffffu, (int)free, 0)) return false;
+      uint8_t* dst = ring.base + (size_t)pos.stage * ring.slot + kWeightBytes;
+      if (kUp) {
+        if (src) bulk_load(dst + lane * kTokPitch, src + (size_t)ch * kChunk, bytes, &c.full[pos.stage]);
+      } else if (lane == 0) {
+        bulk_load(dst, static_cast<const uint8_t*>(a.h) + hidden_at<X>(w.first, w.n, work.chunks, ch, 0), bytes,
                   &c.full[pos.stage]);
+      }
       ++issued;
-      pos.next(a.stages);
+      pos.next(ring.stages);
     }
   }
-  // a block that gives up still waits for the copies it has asked for
-  if ((!ok || c.abort) && lane == 0) {
-    const int n = min(issued, a.stages);
-    for (int i = 0; i < n; ++i) {
-      if (pos.stage == 0) pos.stage = a.stages, pos.phase ^= 1u;
-      --pos.stage;
-      if (!mbar_wait(&c.full[pos.stage], pos.phase, nullptr, a.status, a.limit_ns)) break;
-    }
+  return true;
+}
+
+// A block that gives up still waits for the copies it has asked for.
+__device__ void drain(const FewArgs& a, Ctrl& c, const Ring& ring, Pos pos, int issued) {
+  const int n = min(issued, ring.stages);
+  for (int i = 0; i < n; ++i) {
+    if (pos.stage == 0) pos.stage = ring.stages, pos.phase ^= 1u;
+    --pos.stage;
+    if (!mbar_wait(&c.full[pos.stage], pos.phase, nullptr, a.status, a.limit_ns)) return;
   }
-  __syncwarp();
 }
 
 // Sums of one item into red [parts][kRows][kRedLd]. False: a wait gave up.
-__device__ bool multiply(const Item& w, const FewArgs& a, Ctrl& c, const uint8_t* ring, int slot_bytes, int row_bytes,
-                         Pos& pos, float* red, const __nv_bfloat16*) {
+//
+// bf16: warp w takes bytes 256 w .. 256 w + 255 of the stage's rows, 128 at a
+// time. Rows of weights lie 512 bytes apart, so the two rows that a
+// quarter-warp reads at once would fall on the same banks: odd rows take the
+// two halves of the 128 bytes in the other order.
+template <bool kUp>
+__device__ bool multiply(const Item& w, const FewArgs& a, Ctrl& c, const Ring& ring, int row_bytes, Pos& pos,
+                         float* red, const __nv_bfloat16*) {
+  constexpr int kTiles = kUp ? 2 : 4;  // of 8 columns: a token each, or hi and lo of four
   const int warp = (threadIdx.x >> 5) - 2, lane = threadIdx.x & 31;
-  const int r = lane >> 2;
-  const int t0 = min(r, w.n - 1), t1 = min(r + 8, w.n - 1);
-  float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+  const int r = lane >> 2, q = lane & 3;
+  const bool odd = r & 1;
+  const int cols = kUp ? w.n : 2 * w.n;
+  float acc[kTiles][4];
+#pragma unroll
+  for (int j = 0; j < kTiles; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
   const uint4 zero = make_uint4(0, 0, 0, 0);
   for (int ch = w.c0; ch < w.c1; ++ch) {
     if (!__all_sync(0xffffffffu, mbar_wait(&c.full[pos.stage], pos.phase, &c.abort, a.status, a.limit_ns))) return false;
-    const uint8_t* slot = ring + (size_t)pos.stage * slot_bytes;
-    const int have = chunk_bytes(ch, row_bytes);
+    const uint8_t* slot = ring.base + (size_t)pos.stage * ring.slot;
+    const int have = row_bytes - ch * kChunk;
+    const uint8_t* pw = slot + (warp >> 1) * kRows * kBox + (warp & 1) * 256 + r * kBox + q * 16;
+    const uint8_t* pt = slot + kWeightBytes + warp * 256 + q * 16;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const int off = (warp * 2 + u) * 64 + (lane & 3) * 16;
-      if ((warp * 2 + u) * 64 < have) {
-        const bool in = off < have;
-        const uint8_t* p = slot + off;
-        const uint4 lo = in ? *reinterpret_cast<const uint4*>(p + r * kRowStride) : zero;
-        const uint4 hi = in ? *reinterpret_cast<const uint4*>(p + (r + 8) * kRowStride) : zero;
-        const uint4 b0 = in ? *reinterpret_cast<const uint4*>(p + (kRows + t0) * kRowStride) : zero;
-        mma_block(acc[0], lo, hi, b0);
-        if (w.n > 8) {
-          const uint4 b1 = in ? *reinterpret_cast<const uint4*>(p + (kRows + t1) * kRowStride) : zero;
-          mma_block(acc[1], lo, hi, b1);
+      const int off = warp * 256 + u * 128;
+      if (off < have) {
+        uint4 lo[2], hi[2];
+        lo[0] = *reinterpret_cast<const uint4*>(pw + u * 128 + (odd ? 64 : 0));
+        lo[1] = *reinterpret_cast<const uint4*>(pw + u * 128 + (odd ? 0 : 64));
+        hi[0] = *reinterpret_cast<const uint4*>(pw + u * 128 + 8 * kBox + (odd ? 64 : 0));
+        hi[1] = *reinterpret_cast<const uint4*>(pw + u * 128 + 8 * kBox + (odd ? 0 : 64));
+        const uint4 a0 = odd ? lo[1] : lo[0], a1 = odd ? lo[0] : lo[1];
+        const uint4 b0 = odd ? hi[1] : hi[0], b1 = odd ? hi[0] : hi[1];
+        // the weights end in zeros; the token rows in what was there before
+        const bool in0 = off + q * 16 < have, in1 = off + 64 + q * 16 < have;
+#pragma unroll
+        for (int j = 0; j < kTiles; ++j) {
+          if (j * 8 < cols) {
+            const uint8_t* p = pt + u * 128 + min(j * 8 + r, cols - 1) * kTokPitch;
+            const uint4 t0 = in0 ? *reinterpret_cast<const uint4*>(p) : zero;
+            const uint4 t1 = in1 ? *reinterpret_cast<const uint4*>(p + 64) : zero;
+            mma_block(acc[j], a0, b0, t0);
+            mma_block(acc[j], a1, b1, t1);
+          }
         }
       }
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&c.empty[pos.stage]);
-    pos.next(a.stages);
+    pos.next(ring.stages);
   }
   float* mine = red + warp * kRows * kRedLd;
 #pragma unroll
-  for (int n = 0; n < 2; ++n)
+  for (int j = 0; j < kTiles; ++j) {
+    if (j * 8 < cols) {
+      if (kUp) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (n * 8 < w.n) mine[(r + (i >> 1) * 8) * kRedLd + n * 8 + (lane & 3) * 2 + (i & 1)] = acc[n][i];
+        for (int i = 0; i < 4; ++i) mine[(r + (i >> 1) * 8) * kRedLd + j * 8 + q * 2 + (i & 1)] = acc[j][i];
+      } else {  // columns 2t and 2t + 1: the two terms of token t
+        mine[r * kRedLd + j * 4 + q] = acc[j][0] + acc[j][1];
+        mine[(r + 8) * kRedLd + j * 4 + q] = acc[j][2] + acc[j][3];
+      }
+    }
+  }
   return true;
 }
 
-__device__ bool multiply(const Item& w, const FewArgs& a, Ctrl& c, const uint8_t* ring, int slot_bytes, int row_bytes,
-                         Pos& pos, float* red, const float*) {
+// fp32: warp w takes rows 4 (w / 2) .. + 3 and half of the stage's columns.
+template <bool kUp>
+__device__ bool multiply(const Item& w, const FewArgs& a, Ctrl& c, const Ring& ring, int row_bytes, Pos& pos,
+                         float* red, const float*) {
   const int warp = (threadIdx.x >> 5) - 2, lane = threadIdx.x & 31;
   const int half = warp & 1, r0 = (warp >> 1) * 4;
   float acc[4][16];  // [four tokens][row * 4 + token]
@@ -549,23 +626,28 @@ __device__ bool multiply(const Item& w, const FewArgs& a, Ctrl& c, const uint8_t
     for (int i = 0; i < 16; ++i) acc[g][i] = 0.f;
   for (int ch = w.c0; ch < w.c1; ++ch) {
     if (!__all_sync(0xffffffffu, mbar_wait(&c.full[pos.stage], pos.phase, &c.abort, a.status, a.limit_ns))) return false;
-    const uint8_t* slot = ring + (size_t)pos.stage * slot_bytes;
-    const int off = half * 512 + lane * 16;
-    if (off < chunk_bytes(ch, row_bytes)) {
-      const uint8_t* p = slot + off;
-      float4 wv[4];
+    const uint8_t* slot = ring.base + (size_t)pos.stage * ring.slot;
+    const int have = row_bytes - ch * kChunk;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) wv[i] = *reinterpret_cast<const float4*>(p + (r0 + i) * kRowStride);
+    for (int u = 0; u < 2; ++u) {
+      const int box = half * 2 + u, off = box * kBox + lane * 16;
+      if (off < have) {
+        const uint8_t* pw = slot + box * kRows * kBox + r0 * kBox + lane * 16;
+        const uint8_t* pt = slot + kWeightBytes + off;
+        float4 wv[4];
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        if (g * 4 < w.n) {
+        for (int i = 0; i < 4; ++i) wv[i] = *reinterpret_cast<const float4*>(pw + i * kBox);
 #pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            const float4 b = *reinterpret_cast<const float4*>(p + (kRows + g * 4 + t) * kRowStride);
+        for (int g = 0; g < 4; ++g) {
+          if (g * 4 < w.n) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              float& s = acc[g][i * 4 + t];
-              s = fmaf(wv[i].w, b.w, fmaf(wv[i].z, b.z, fmaf(wv[i].y, b.y, fmaf(wv[i].x, b.x, s))));
+            for (int t = 0; t < 4; ++t) {
+              const float4 b = *reinterpret_cast<const float4*>(pt + (g * 4 + t) * kTokPitch);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                float& s = acc[g][i * 4 + t];
+                s = fmaf(wv[i].w, b.w, fmaf(wv[i].z, b.z, fmaf(wv[i].y, b.y, fmaf(wv[i].x, b.x, s))));
+              }
             }
           }
         }
@@ -573,7 +655,7 @@ __device__ bool multiply(const Item& w, const FewArgs& a, Ctrl& c, const uint8_t
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&c.empty[pos.stage]);
-    pos.next(a.stages);
+    pos.next(ring.stages);
   }
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
@@ -589,6 +671,13 @@ __device__ __forceinline__ float silu_of(float z, const __nv_bfloat16*) { return
 __device__ __forceinline__ float silu_of(float z, const float*) { return z / (1.f + expf(-z)); }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
+// A hidden value into its row, and what the row leaves of it into the next.
+__device__ __forceinline__ void put_hidden(uint8_t* p, float v, const __nv_bfloat16*) {
+  const __nv_bfloat16 hi = __float2bfloat16_rn(v);
+  *reinterpret_cast<__nv_bfloat16*>(p) = hi;
+  *reinterpret_cast<__nv_bfloat16*>(p + kTokPitch) = __float2bfloat16_rn(v - __bfloat162float(hi));
+}
+__device__ __forceinline__ void put_hidden(uint8_t* p, float v, const float*) { *reinterpret_cast<float*>(p) = v; }
 
 template <typename X>
 __device__ __forceinline__ float sum_parts(const float* red, int row, int n) {
@@ -599,8 +688,9 @@ __device__ __forceinline__ float sum_parts(const float* red, int row, int n) {
 }
 
 template <typename X, bool kUp>
-__device__ void consume(const FewArgs& a, Ctrl& c, const uint8_t* ring, int slot_bytes, float* red2) {
+__device__ void consume(const FewArgs& a, Ctrl& c, const Ring& ring, float* red2) {
   const Work<X, kUp> work(a, c.plan);
+  const int hid_chunks = (a.I * (int)sizeof(X) + kChunk - 1) / kChunk;
   const int K = kUp ? a.d : a.I;
   const int tid = threadIdx.x - 64;
   const int R = a.T * a.k;
@@ -610,15 +700,15 @@ __device__ void consume(const FewArgs& a, Ctrl& c, const uint8_t* ring, int slot
     const Item w = work.item(i, c.plan);
     float* red = red2 + buf * red_floats<X>();
     buf ^= 1;
-    const bool ok = multiply(w, a, c, ring, slot_bytes, K * (int)sizeof(X), pos, red, static_cast<const X*>(nullptr));
+    const bool ok = multiply<kUp>(w, a, c, ring, K * (int)sizeof(X), pos, red, static_cast<const X*>(nullptr));
     if (!math_sync_all(ok)) break;
     if (kUp) {
-      // the hidden values, rounded to the layer's type as the larger batches' are
       const int u = tid & 7, n = tid >> 3, unit = w.blk * 8 + u;
       if (n < w.n && unit < a.I) {
         const float g = sum_parts<X>(red, u, n), up = sum_parts<X>(red, 8 + u, n);
-        put(static_cast<X*>(a.h) + (size_t)(w.first + n) * a.I + unit,
-            silu_of(g, static_cast<const X*>(nullptr)) * up);
+        const int ch = unit * (int)sizeof(X) / kChunk, at = unit * (int)sizeof(X) % kChunk;
+        put_hidden(static_cast<uint8_t*>(a.h) + hidden_at<X>(w.first, w.n, hid_chunks, ch, n * Traits<X>::kHid) + at,
+                   silu_of(g, static_cast<const X*>(nullptr)) * up, static_cast<const X*>(nullptr));
       }
     } else {
       const int r = tid & 15, n = tid >> 4, col = w.blk * kRows + r;
@@ -645,20 +735,27 @@ __device__ void consume(const FewArgs& a, Ctrl& c, const uint8_t* ring, int slot
 }
 
 template <typename X, bool kUp>
-__device__ void stream(const FewArgs& a, Ctrl& c, uint8_t* ring, float* red) {
-  const int slot_bytes = slot_rows<X>(a.T) * kRowStride;
-  const int warp = threadIdx.x >> 5;
-  if (warp == 0)
-    produce<X, kUp, false>(a, c, ring, slot_bytes);
-  else if (warp == 1)
-    produce<X, kUp, true>(a, c, ring, slot_bytes);
-  else
-    consume<X, kUp>(a, c, ring, slot_bytes, red);
+__device__ void stream(const FewMaps& maps, const FewArgs& a, Ctrl& c, uint8_t* smem_ring, float* red) {
+  const Ring ring = ring_of<X, kUp>(smem_ring, c.plan);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  Pos pos;
+  int issued = 0;
+  if (warp == 0) {
+    if (lane == 0 && (!produce_weights<X, kUp>(maps, a, c, ring, pos, issued) || c.abort))
+      drain(a, c, ring, pos, issued);
+    __syncwarp();
+  } else if (warp == 1) {
+    const bool ok = produce_tokens<X, kUp>(a, c, ring, pos, issued);
+    if (lane == 0 && (!ok || c.abort)) drain(a, c, ring, pos, issued);
+    __syncwarp();
+  } else {
+    consume<X, kUp>(a, c, ring, red);
+  }
 }
 
-__device__ __forceinline__ void init_ctrl(Ctrl& c, int stages) {
+__device__ __forceinline__ void init_ctrl(Ctrl& c) {
   if (threadIdx.x == 0) {
-    for (int s = 0; s < stages; ++s) {
+    for (int s = 0; s < kMaxStages; ++s) {
       mbar_init(&c.full[s], 2);
       mbar_init(&c.empty[s], kMathWarps);
     }
@@ -670,25 +767,25 @@ __device__ __forceinline__ void init_ctrl(Ctrl& c, int stages) {
 template <typename X>
 __device__ __forceinline__ void carve(uint8_t* smem, Ctrl** c, float** red, uint8_t** ring) {
   *c = reinterpret_cast<Ctrl*>(smem);
-  *red = reinterpret_cast<float*>(smem + (sizeof(Ctrl) + 15) / 16 * 16);
+  *red = reinterpret_cast<float*>(smem + (sizeof(Ctrl) + 127) / 128 * 128);
   *ring = reinterpret_cast<uint8_t*>(*red + 2 * red_floats<X>());
 }
 
 template <typename X>
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1) few_up_kernel(const FewArgs a) {
-  extern __shared__ __align__(16) uint8_t smem[];
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1) few_up_kernel(const __grid_constant__ FewMaps maps, const FewArgs a) {
+  extern __shared__ __align__(128) uint8_t smem[];
   Ctrl* c;
   float* red;
   uint8_t* ring;
   carve<X>(smem, &c, &red, &ring);
-  init_ctrl(*c, a.stages);
+  init_ctrl(*c);
   float* part = reinterpret_cast<float*>(ring);                     // [kCluster][T][E]
   float* scratch = part + (size_t)kCluster * a.T * a.E;             // [kWarps][kPassE][16]
   const int rank = (int)cluster_ctarank();
   cluster_sync();  // the peers' shared memory exists
   pdl_wait();
   pdl_trigger();
-  // this CTA's columns, in units of 16 bytes of both types
+  // this CTA's columns
   const int unit = 32, units = (a.d + unit - 1) / unit;
   const int c0 = min(a.d, rank * units / kCluster * unit), c1 = min(a.d, (rank + 1) * units / kCluster * unit);
   logits_part(static_cast<const X*>(a.x), static_cast<const X*>(a.wr), a.T, a.d, a.E, c0, c1, scratch, part, rank);
@@ -703,17 +800,17 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1) 
   }
   fence_async();  // the ring's memory was written above, and is next by the copies
   __syncthreads();
-  stream<X, true>(a, *c, ring, red);
+  stream<X, true>(maps, a, *c, ring, red);
 }
 
 template <typename X>
-__global__ void __launch_bounds__(kThreads, 1) few_down_kernel(const FewArgs a) {
-  extern __shared__ __align__(16) uint8_t smem[];
+__global__ void __launch_bounds__(kThreads, 1) few_down_kernel(const __grid_constant__ FewMaps maps, const FewArgs a) {
+  extern __shared__ __align__(128) uint8_t smem[];
   Ctrl* c;
   float* red;
   uint8_t* ring;
   carve<X>(smem, &c, &red, &ring);
-  init_ctrl(*c, a.stages);
+  init_ctrl(*c);
   pdl_wait();
   pdl_trigger();
   const int i = threadIdx.x;
@@ -729,7 +826,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_down_kernel(const FewArgs a) 
   __syncthreads();
   make_plan(c->plan, c->idx, c->gate, a.T, a.E, a.k);
   fence_async();  // few_up's hidden rows are read by the copies
-  stream<X, false>(a, *c, ring, red);
+  stream<X, false>(maps, a, *c, ring, red);
 }
 
 // What a launch needs to know of a device, found once.
@@ -775,22 +872,17 @@ cudaError_t device_info(Device* out) {
 }
 
 template <typename X>
-cudaError_t launch(FewArgs a, cudaStream_t stream) {
+cudaError_t launch(const FewMaps& m, const FewArgs& a, cudaStream_t stream) {
+  // the routing's scratch lies where the ring is, and every ring has two stages
+  constexpr int kRing = kSmemTotal - fixed_bytes<X>();
+  static_assert(4 * (kCluster * kFewTokens * kMaxExperts + kWarps * kPassE * kFewTokens) <= kRing, "routing scratch");
+  static_assert(2 * (kWeightBytes + Traits<X>::kHid * kFewTokens * kTokPitch + 128) <= kRing, "ring");
   Device dev;
   cudaError_t err = device_info<X>(&dev);
   if (err != cudaSuccess) return err;
-  const int slot = slot_rows<X>(a.T) * kRowStride;
-  a.stages = (kSmemTotal - fixed_bytes<X>()) / slot;
-  if (a.stages > kMaxStages) a.stages = kMaxStages;
-  // the routing's scratch lies where the ring is
-  static_assert(4 * (kCluster * kFewTokens * kMaxExperts + kWarps * kPassE * kFewTokens) <=
-                    5 * (kRows + kFewTokens) * kRowStride,
-                "routing scratch");
-  const size_t routing = 4 * ((size_t)kCluster * a.T * a.E + (size_t)kWarps * kPassE * kFewTokens);
-  if (a.stages < 2 || routing > (size_t)(kSmemTotal - fixed_bytes<X>())) return cudaErrorInvalidConfiguration;
-  err = launch_pdl(few_up_kernel<X>, dim3(dev.clusters * kCluster), dim3(kThreads), kSmemTotal, stream, a);
+  err = launch_pdl(few_up_kernel<X>, dim3(dev.clusters * kCluster), dim3(kThreads), kSmemTotal, stream, m, a);
   if (err != cudaSuccess) return err;
-  return launch_pdl(few_down_kernel<X>, dim3(dev.sms), dim3(kThreads), kSmemTotal, stream, a);
+  return launch_pdl(few_down_kernel<X>, dim3(dev.sms), dim3(kThreads), kSmemTotal, stream, m, a);
 }
 
 }  // namespace
@@ -803,14 +895,15 @@ FewWorkspace few_layout(int T, int d, int k, int I, moe_dtype dtype) {
   w.split = R > 0 && 256 / R < kFewMaxSplit ? (int)(256 / R) : kFewMaxSplit;
   size_t o = 0;
   w.done = o; o = align256(o + 4 * (size_t)((d + kRows - 1) / kRows));
-  w.h = o;    o = align256(o + el * R * (size_t)I);
+  const size_t chunks = (el * (size_t)I + kChunk - 1) / kChunk;
+  w.h = o;    o = align256(o + R * chunks * kTokPitch * (dtype == MOE_BF16 ? Traits<__nv_bfloat16>::kHid : 1));
   w.y = o;    o = align256(o + 4 * (size_t)w.split * R * (size_t)d);
   w.total = o;
   return w;
 }
 
-cudaError_t launch_few(moe_dtype dtype, FewArgs a, cudaStream_t stream) {
-  return dtype == MOE_BF16 ? launch<__nv_bfloat16>(a, stream) : launch<float>(a, stream);
+cudaError_t launch_few(moe_dtype dtype, const FewMaps& m, const FewArgs& a, cudaStream_t stream) {
+  return dtype == MOE_BF16 ? launch<__nv_bfloat16>(m, a, stream) : launch<float>(m, a, stream);
 }
 
 }  // namespace moe

@@ -67,7 +67,12 @@ moe_status moe_forward_few(const void* x, const void* w_router, const float* b_r
   a.split = l.split;
   a.status = status_dev;
   a.limit_ns = kWaitLimitNs;
-  const cudaError_t err = launch_few(dtype, a, stream);
+  FewMaps m;
+  if (!make_tmap_few(&m.wg, w_gate, dtype, (uint64_t)E * I, (uint64_t)d, 8) ||
+      !make_tmap_few(&m.wu, w_up, dtype, (uint64_t)E * I, (uint64_t)d, 8) ||
+      !make_tmap_few(&m.wd, w_down, dtype, (uint64_t)E * d, (uint64_t)I, 16))
+    return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed (driver entry point unavailable or bad pointer)");
+  const cudaError_t err = launch_few(dtype, m, a, stream);
   return err == cudaSuccess ? MOE_OK : fail_cuda(err, "few-token kernels");
 }
 

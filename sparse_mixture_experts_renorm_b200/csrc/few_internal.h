@@ -7,12 +7,13 @@
 namespace moe {
 
 constexpr int kFewTokens = MOE_FEW_TOKENS;  // two n8 tiles of an mma.sync step
-constexpr int kFewMaxSplit = 8;   // parts of a down product's columns
+constexpr int kFewMaxSplit = 8;                // parts of a down product's columns
+constexpr int kFewTokPitch = 2048 + 64;        // bytes between token rows in shared memory and of hidden rows
 
 // Byte offsets inside the workspace.
 struct FewWorkspace {
   size_t done;   // int32 [blocks of 16 output columns] finished parts
-  size_t h;      // dtype [T*k, I] hidden rows in expert order
+  size_t h;      // hidden rows by expert and chunk of columns (few.cu, hidden_at)
   size_t y;      // fp32  [split, T*k, d] gated expert outputs
   size_t total;
   int split;     // parts that y has room for
@@ -31,12 +32,17 @@ struct FewArgs {
   void* h;
   float* y;
   int split;        // parts that y has room for
-  int stages;       // ring stages, set by the launcher
   int32_t* status;
   uint64_t limit_ns;
 };
 
+// Weight rows in boxes of 512 bytes: 8 rows of gate and up, 16 of down.
+struct FewMaps {
+  CUtensorMap wg, wu, wd;
+};
+bool make_tmap_few(CUtensorMap* map, const void* base, moe_dtype dtype, uint64_t rows, uint64_t cols, uint32_t box_rows);
+
 FewWorkspace few_layout(int T, int d, int k, int I, moe_dtype dtype);
-cudaError_t launch_few(moe_dtype dtype, FewArgs a, cudaStream_t stream);
+cudaError_t launch_few(moe_dtype dtype, const FewMaps& m, const FewArgs& a, cudaStream_t stream);
 
 }  // namespace moe
