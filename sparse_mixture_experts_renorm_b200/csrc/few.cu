@@ -32,21 +32,23 @@
 namespace moe {
 namespace {
 
-constexpr int kWarps = 10;               // 0: weights, 1: token rows, 2..9: products
-constexpr int kThreads = 32 * kWarps;
 constexpr int kMathWarps = 8;
 constexpr int kMath = 32 * kMathWarps;
+constexpr int kGroupWarps = 2 + kMathWarps;  // a group: 0: weights, 1: token rows, 2..9: products
+constexpr int kMaxGroups = 2;
 constexpr int kRows = 16;                // weight rows of a stage
 constexpr int kBox = 512;                // bytes of a row in one tile load
-constexpr int kBoxes = 4;                // tile loads side by side in a stage
+constexpr int kBoxes = 2;                // tile loads side by side in a stage
 constexpr int kChunk = kBox * kBoxes;    // bytes of a row in a stage
 constexpr int kWeightBytes = kRows * kChunk;
 constexpr int kTokPitch = kFewTokPitch;  // bytes between token rows: two rows of a quarter-warp's load on different banks
 static_assert(kTokPitch == kChunk + 64, "pitch");
-constexpr int kMaxStages = 8;
+constexpr int kMaxStages = 10;           // of a group
+constexpr int kAhead = 16;               // stages of a block brought to L2 ahead of time: 38 MB on 148 SMs
 constexpr int kMaxRows = kFewTokens * kMaxTopK;
 constexpr int kCluster = 4;              // CTAs that share one routing
 constexpr int kPassE = 64;               // experts whose logits a warp holds at a time
+constexpr int kPassLd = kPassE + 4;      // 2 kPassLd % 32 == 8: an mma.sync result's lanes on different banks
 constexpr int kSmemTotal = 227 * 1024;
 
 struct Plan {
@@ -60,14 +62,23 @@ struct Plan {
   int slot[kMaxExperts];
 };
 
-struct Ctrl {
-  uint64_t full[kMaxStages];   // both producers' bytes
+// One group's barriers and lists.
+struct Group {
+  uint64_t full[kMaxStages];   // the producers' bytes
   uint64_t empty[kMaxStages];  // the math warps
+  int item[kMaxStages];        // few_down: the item that a stage begins, or -1: there are no more
+  int n_last;
+  int blk[kMath];              // few_down: blocks of output columns of the items since the last join
+  int last[kMath];             // and those of them to add up
+};
+
+struct Ctrl {
+  Group group[kMaxGroups];
   volatile int abort;
-  int last;
   int idx[kMaxRows];
   float gate[kMaxRows];
-  float red[kWarps];
+  float bias[kMaxExperts];
+  float red[kMaxGroups * kGroupWarps];
   Plan plan;
 };
 
@@ -77,35 +88,45 @@ struct Ctrl {
 // 2^-17: rounded to one, it would double the error that the output's own
 // rounding makes, and the second term costs only shared memory and issue slots
 // (both are columns of the same mma.sync while an expert has few tokens).
+// kGroups: independent pipelines of a block, with half of the ring each: while
+// one adds up its partial sums, the other multiplies. The fp32 products hold
+// too many sums in registers for a second one.
 template <typename X>
 struct Traits;
 template <>
 struct Traits<__nv_bfloat16> {
-  static constexpr int kParts = kMathWarps, kHid = 2;
+  static constexpr int kParts = kMathWarps, kHid = 2, kGroups = 2;
 };
 template <>
 struct Traits<float> {
-  static constexpr int kParts = 2, kHid = 1;
+  static constexpr int kParts = 2, kHid = 1, kGroups = 1;
 };
 constexpr int kRedLd = kFewTokens + 1;
 template <typename X>
 constexpr int red_floats() { return Traits<X>::kParts * kRows * kRedLd; }
 template <typename X>
-constexpr int fixed_bytes() { return (int)((sizeof(Ctrl) + 127) / 128 * 128 + 2 * red_floats<X>() * 4); }
+constexpr int threads() { return Traits<X>::kGroups * kGroupWarps * 32; }
+template <typename X>
+constexpr int fixed_bytes() {
+  return (int)((sizeof(Ctrl) + 127) / 128 * 128 + 2 * Traits<X>::kGroups * red_floats<X>() * 4);
+}
 
-// The ring's shape follows from the most tokens that an expert got.
+// The rings' shape follows from the most tokens that an expert got: two groups
+// where each still has three stages.
 struct Ring {
   uint8_t* base;
-  int slot, stages;
+  int slot, stages, groups;
 };
 template <typename X, bool kUp>
-__device__ __forceinline__ Ring ring_of(uint8_t* base, const Plan& p) {
+__device__ __forceinline__ Ring ring_of(uint8_t* base, const Plan& p, int group) {
+  constexpr int kBytes = kSmemTotal - fixed_bytes<X>();
   int rows = kUp ? p.most : p.most * Traits<X>::kHid;
   if (sizeof(X) == 4) rows = (rows + 3) & ~3;  // fp32 multiplies four token rows at a time
   Ring r;
-  r.base = base;
   r.slot = (kWeightBytes + rows * kTokPitch + 127) & ~127;
-  r.stages = min(kMaxStages, (kSmemTotal - fixed_bytes<X>()) / r.slot);
+  r.groups = Traits<X>::kGroups == 2 && 6 * r.slot <= kBytes ? 2 : 1;
+  r.stages = min(kMaxStages, kBytes / (r.groups * r.slot));
+  r.base = base + (size_t)group * r.stages * r.slot;
   return r;
 }
 
@@ -115,18 +136,25 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
       "l"(src), "r"(bytes), "r"(smem_u32(bar))
       : "memory");
 }
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int x, int y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y)
+               : "memory");
+}
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
-__device__ __forceinline__ void math_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kMath) : "memory"); }
+__device__ __forceinline__ void math_sync(int group) {
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(kMath) : "memory");
+}
 // The same, and whether any thread of it said no: all leave together.
-__device__ __forceinline__ bool math_sync_all(bool ok) {
+__device__ __forceinline__ bool math_sync_all(int group, bool ok) {
   uint32_t any;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.eq.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, 1, %2, p;\n\t"
+      "barrier.cta.red.or.pred q, %3, %2, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(any)
-      : "r"((uint32_t)ok), "n"(kMath)
+      : "r"((uint32_t)ok), "n"(kMath), "r"(1 + group)
       : "memory");
   return any == 0;
 }
@@ -171,7 +199,7 @@ __device__ __forceinline__ float reduce_many(float (&v)[N]) {
 // the block. A token names an expert once.
 __device__ void make_plan(Plan& p, const int* idx, const float* gate, int T, int E, int k) {
   const int R = T * k;
-  for (int e = threadIdx.x; e < E; e += kThreads) p.mask[e] = 0;
+  for (int e = threadIdx.x; e < E; e += blockDim.x) p.mask[e] = 0;
   __syncthreads();
   const int i = threadIdx.x;
   if (i < R) atomicOr(&p.mask[idx[i]], 1u << (i / k));
@@ -218,15 +246,16 @@ __device__ void make_plan(Plan& p, const int* idx, const float* gate, int T, int
 // ---------------------------------------------------------------- routing --
 
 // Partial logits of all T tokens and E experts over columns [c0, c1): warp
-// sums in scratch [kWarps][kPassE][T], added up in warp order into every
-// cluster CTA's part[rank][T][E].
+// sums in scratch [kWarps][T][kPassLd], added up in warp order into every
+// cluster CTA's part[rank][T][E]. bias [E] is added to one CTA's.
 template <typename X>
 __device__ void logits_part(const X* __restrict__ x, const X* __restrict__ wr, int T, int d, int E, int c0, int c1,
-                            float* scratch, float* part, int rank) {
+                            const float* bias, float* scratch, float* part, int rank) {
+  constexpr int kWarps = threads<X>() / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int e0 = 0; e0 < E; e0 += kPassE) {
     const int ne = min(kPassE, E - e0);
-    float* mine = scratch + warp * kPassE * kFewTokens;
+    float* mine = scratch + warp * kFewTokens * kPassLd;
     if constexpr (sizeof(X) == 2) {
       float acc[kPassE / 16][2][4];
 #pragma unroll
@@ -237,7 +266,7 @@ __device__ void logits_part(const X* __restrict__ x, const X* __restrict__ wr, i
           for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
       const int r = lane >> 2;
       const uint4 zero = make_uint4(0, 0, 0, 0);
-#pragma unroll 2
+#pragma unroll 1
       for (int c = c0 + warp * 32; c < c1; c += kWarps * 32) {
         const int col = c + (lane & 3) * 8;
         const bool in = col < c1;
@@ -264,7 +293,7 @@ __device__ void logits_part(const X* __restrict__ x, const X* __restrict__ wr, i
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int e = m * 16 + r + (i >> 1) * 8, t = n * 8 + (lane & 3) * 2 + (i & 1);
-            if (m * 16 < ne) mine[e * kFewTokens + t] = acc[m][n][i];
+            if (m * 16 < ne) mine[t * kPassLd + e] = acc[m][n][i];
           }
     } else {
       for (int e = 0; e < ne; e += 4)
@@ -286,106 +315,104 @@ __device__ void logits_part(const X* __restrict__ x, const X* __restrict__ wr, i
             }
           }
           const float s = reduce_many(v);
-          if ((lane & 1) == 0) mine[(e + (lane >> 3)) * kFewTokens + t + ((lane >> 1) & 3)] = s;
+          if ((lane & 1) == 0) mine[(t + ((lane >> 1) & 3)) * kPassLd + e + (lane >> 3)] = s;
         }
     }
     __syncthreads();
-    const int peers = kCluster;
-    for (int i = threadIdx.x; i < ne * T; i += kThreads) {
+    for (int i = threadIdx.x; i < ne * T; i += blockDim.x) {
       const int t = i / ne, e = i - t * ne;
-      float s = 0.f;
+      float s = rank == 0 ? bias[e0 + e] : 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) s += scratch[(w * kPassE + e) * kFewTokens + t];
+      for (int w = 0; w < kWarps; ++w) s += scratch[(w * kFewTokens + t) * kPassLd + e];
       float* dst = part + ((size_t)rank * T + t) * E + e0 + e;
-      for (int c = 0; c < peers; ++c) store_cluster(map_to_cta(dst, c), s);
+      for (int c = 0; c < kCluster; ++c) store_cluster(map_to_cta(dst, c), s);
     }
     __syncthreads();
   }
 }
 
+// A float's bits in an order that integers have: -inf < ... < inf, NaN below
+// them all, 0 for none.
+__device__ __forceinline__ uint32_t rank_key(float v) {
+  const uint32_t b = __float_as_uint(v);
+  return v != v ? 1u : b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float key_value(uint32_t key) {
+  return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
+}
+
 // Softmax, the k best (ties to the lower index) and their gates, one warp a
-// token. part [kCluster][T][E]; the probabilities replace part[0].
-template <typename X>
+// token. part [kCluster][T][E]; the logits replace part[0], and then the
+// probabilities if the statistic is wanted. The loops stay rolled: the code
+// runs once, and fetching it is what it would wait for.
 __device__ void choose(const FewArgs& a, float* part, Ctrl& c, bool write) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int kPer = kMaxExperts / 32;
   const int T = a.T, E = a.E, k = a.k;
-  for (int t = warp; t < T; t += kWarps) {
-    float v[kPer];
-    float m = -INFINITY;
+  for (int t = warp; t < T; t += blockDim.x / 32) {
+    float* row = part + (size_t)t * E;
     bool finite = true;
+    uint32_t best = 0;
+#pragma unroll 1
+    for (int e = lane; e < E; e += 32) {
+      float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int e = lane + 32 * i;
-      v[i] = -INFINITY;
-      if (e < E) {
-        float s = 0.f;
-#pragma unroll
-        for (int q = 0; q < kCluster; ++q) s += part[((size_t)q * T + t) * E + e];
-        if (a.br) s += a.br[e];
-        finite = finite && isfinite(s);
-        v[i] = s;
-        m = fmaxf(m, s);
-      }
+      for (int q = 0; q < kCluster; ++q) s += row[(size_t)q * T * E + e];
+      finite = finite && isfinite(s);
+      row[e] = s;
+      best = max(best, rank_key(s));
     }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float m = key_value(__reduce_max_sync(0xffffffffu, best));
     float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) sum += lane + 32 * i < E ? expf(v[i] - m) : 0.f;
+#pragma unroll 1
+    for (int e = lane; e < E; e += 32) sum += expf(row[e] - m);
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (lane + 32 * i < E) part[(size_t)t * E + lane + 32 * i] = expf(v[i] - m) / sum;
-    if (!__all_sync(0xffffffffu, finite) && lane == 0 && write) atomicOr(a.status, MOE_DEV_NONFINITE);
+    if (write && !__all_sync(0xffffffffu, finite) && lane == 0) atomicOr(a.status, MOE_DEV_NONFINITE);
     // k rounds of an arg-max over the logits, which rank as their exact
     // probabilities do; NaN ranks lowest, so that every token still gets k
     // different experts
     uint32_t taken = 0;
-    float mine = 0.f, total = 0.f;
-    int mine_e = 0;
+    float l = -INFINITY;
+    int mine = 0;
+#pragma unroll 1
     for (int j = 0; j < k; ++j) {
-      float bv = -INFINITY;
+      best = 0;
       int be = 0x7fffffff;
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int e = lane + 32 * i;
-        if (e < E && !((taken >> i) & 1u)) {
-          const float l = v[i] != v[i] ? -INFINITY : v[i];
-          if (l > bv || (l == bv && e < be)) bv = l, be = e;
-        }
+#pragma unroll 1
+      for (int e = lane, i = 0; e < E; e += 32, ++i) {
+        const uint32_t key = (taken >> i) & 1u ? 0u : rank_key(row[e]);
+        if (key > best) best = key, be = e;
       }
-#pragma unroll
-      for (int o = 16; o; o >>= 1) {
-        const float ov = __shfl_xor_sync(0xffffffffu, bv, o);
-        const int oe = __shfl_xor_sync(0xffffffffu, be, o);
-        if (ov > bv || (ov == bv && oe < be)) bv = ov, be = oe;
-      }
-      if ((be & 31) == lane) taken |= 1u << (be >> 5);
-      const float p = expf(bv - m) / sum;
-      total += p;
-      if (lane == j) mine = p, mine_e = be;
+      const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+      const int e = __reduce_min_sync(0xffffffffu, best == top ? be : 0x7fffffff);
+      if ((e & 31) == lane) taken |= 1u << (e >> 5);
+      if (lane == j) l = key_value(top), mine = e;
     }
+    const float p = expf(l - m) / sum;
+    float total = lane < k ? p : 0.f;
+#pragma unroll
+    for (int o = 4; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     if (lane < k) {
-      const float g = !a.renorm ? mine : total > 0.f ? mine / total : 1.f / (float)k;
-      c.idx[t * k + lane] = mine_e;
+      const float g = !a.renorm ? p : total > 0.f ? p / total : 1.f / (float)k;
+      c.idx[t * k + lane] = mine;
       c.gate[t * k + lane] = g;
       if (write) {
-        a.idx[(size_t)t * k + lane] = mine_e;
+        a.idx[(size_t)t * k + lane] = mine;
         a.gate[(size_t)t * k + lane] = g;
       }
     }
+    if (write && a.aux)
+      for (int e = lane; e < E; e += 32) row[e] = expf(row[e] - m) / sum;
   }
 }
 
 // counts and the load-balancing statistic, by one block; prob [T][E].
 __device__ void statistics(const FewArgs& a, const float* prob, Ctrl& c) {
-  for (int e = threadIdx.x; e < a.E; e += kThreads)
+  for (int e = threadIdx.x; e < a.E; e += blockDim.x)
     if (a.counts) a.counts[e] = __popc(c.plan.mask[e]);
   if (!a.aux) return;
   float s = 0.f;
-  for (int e = threadIdx.x; e < a.E; e += kThreads) {
+  for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
     float p = 0.f;
     for (int t = 0; t < a.T; ++t) p += prob[(size_t)t * a.E + e];
     s += (float)__popc(c.plan.mask[e]) * p;
@@ -396,7 +423,7 @@ __device__ void statistics(const FewArgs& a, const float* prob, Ctrl& c) {
   __syncthreads();
   if (threadIdx.x == 0) {
     float sum = 0.f;
-    for (int w = 0; w < kWarps; ++w) sum += c.red[w];
+    for (int w = 0; w < (int)blockDim.x / 32; ++w) sum += c.red[w];
     *a.aux = sum * (float)a.E / ((float)(a.T * a.k) * (float)a.T);
   }
 }
@@ -416,24 +443,24 @@ struct Item {
 template <typename X, bool kUp>
 struct Work {
   int n_blk, split, chunks, total;
-  __device__ Work(const FewArgs& a, const Plan& p) {
+  __device__ Work(const FewArgs& a, int n_act, int grid) {
     const int K = kUp ? a.d : a.I;
     chunks = (K * (int)sizeof(X) + kChunk - 1) / kChunk;
     n_blk = kUp ? (a.I + 7) / 8 : (a.d + 15) / 16;
     split = 1;
-    const int items = p.n_act * n_blk;
+    const int items = n_act * n_blk;
     if (!kUp) {
       // the parts that leave the busiest block the fewest chunks; a finer
       // split has to gain 3 %
-      float best = (float)((items + gridDim.x - 1) / gridDim.x) * (float)chunks;
+      float best = (float)((items + grid - 1) / grid) * (float)chunks;
       for (int q = 2; q <= min(a.split, chunks); ++q) {
-        const float t = (float)((items * q + gridDim.x - 1) / gridDim.x) * (float)((chunks + q - 1) / q);
+        const float t = (float)((items * q + grid - 1) / grid) * (float)((chunks + q - 1) / q);
         if (t < 0.97f * best) best = t, split = q;
       }
     }
     total = items * split;
   }
-  __device__ __forceinline__ Item item(int i, const Plan& p) const {
+  __device__ __forceinline__ Item item(int i) const {
     Item w;
     const int q = i / split;
     w.part = i - q * split;
@@ -441,6 +468,10 @@ struct Work {
     w.blk = q - w.s * n_blk;
     w.c0 = w.part * chunks / split;
     w.c1 = (w.part + 1) * chunks / split;
+    return w;
+  }
+  __device__ __forceinline__ Item item(int i, const Plan& p) const {
+    Item w = item(i);
     w.first = p.base[w.s];
     w.n = p.base[w.s + 1] - w.first;
     return w;
@@ -465,31 +496,69 @@ __device__ __forceinline__ size_t hidden_at(int first, int n, int chunks, int ch
   return (((size_t)first * chunks + (size_t)n * chunk) * kHid + row) * kTokPitch;
 }
 
-// The weights' producer: one lane. Rows past the last block's are read from
-// the next expert, or as zeros, and go into sums that nobody takes.
+// Asks for the weights of block `block`'s first stages to be brought to L2.
 template <typename X, bool kUp>
-__device__ bool produce_weights(const FewMaps& maps, const FewArgs& a, Ctrl& c, const Ring& ring, Pos& pos, int& issued) {
-  const Work<X, kUp> work(a, c.plan);
+__device__ void prefetch_weights(const FewMaps& maps, const FewArgs& a, const int* expert, int n_act, int block,
+                                 int grid) {
+  const Work<X, kUp> work(a, n_act, grid);
   const int row_bytes = (kUp ? a.d : a.I) * (int)sizeof(X);
-  for (int i = blockIdx.x; i < work.total; i += gridDim.x) {
-    const Item w = work.item(i, c.plan);
-    const int e = c.plan.expert[w.s];
+  int n = 0;
+  for (int i = block; i < work.total; i += grid) {
+    const Item w = work.item(i);
+    const int e = expert ? expert[w.s] : w.s;
     const int row = kUp ? e * a.I + w.blk * 8 : e * a.d + w.blk * kRows;
     for (int ch = w.c0; ch < w.c1; ++ch) {
-      if (!mbar_wait(&c.empty[pos.stage], pos.phase ^ 1u, &c.abort, a.status, a.limit_ns)) return false;
-      uint8_t* dst = ring.base + (size_t)pos.stage * ring.slot;
-      const int boxes = min(kBoxes, (row_bytes - ch * kChunk + kBox - 1) / kBox);
-      mbar_arrive_expect_tx(&c.full[pos.stage], (uint32_t)(boxes * kRows * kBox));
-      for (int b = 0; b < boxes; ++b) {
-        const int col = (ch * kChunk + b * kBox) / (int)sizeof(X);
-        uint8_t* to = dst + b * kRows * kBox;
-        if (kUp) {  // rows 0..7: gate rows of 8 hidden units, 8..15: their up rows
-          tma_load_2d(to, &maps.wg, &c.full[pos.stage], col, row);
-          tma_load_2d(to + 8 * kBox, &maps.wu, &c.full[pos.stage], col, row);
+      if (n++ == kAhead) return;
+      for (int at = ch * kChunk; at < min(row_bytes, (ch + 1) * kChunk); at += kBox) {
+        const int col = at / (int)sizeof(X);
+        if (kUp) {
+          tma_prefetch_2d(&maps.wg, col, row);
+          tma_prefetch_2d(&maps.wu, col, row);
         } else {
-          tma_load_2d(to, &maps.wd, &c.full[pos.stage], col, row);
+          tma_prefetch_2d(&maps.wd, col, row);
         }
       }
+    }
+  }
+}
+
+// Asks for a stage of weights. Rows past the last block's are read from the
+// next expert, or as zeros, and go into sums that nobody takes. Returns bytes.
+template <typename X, bool kUp>
+__device__ __forceinline__ uint32_t weight_bytes(int chunk, int row_bytes) {
+  return (uint32_t)(min(kBoxes, (row_bytes - chunk * kChunk + kBox - 1) / kBox) * kRows * kBox);
+}
+template <typename X, bool kUp>
+__device__ __forceinline__ void load_weights(const FewMaps& maps, uint8_t* dst, uint64_t* bar, int chunk, int row,
+                                             int row_bytes) {
+#pragma unroll
+  for (int b = 0; b < kBoxes; ++b) {
+    const int at = chunk * kChunk + b * kBox, col = at / (int)sizeof(X);
+    uint8_t* to = dst + b * kRows * kBox;
+    if (at < row_bytes) {
+      if (kUp) {  // rows 0..7: gate rows of 8 hidden units, 8..15: their up rows
+        tma_load_2d(to, &maps.wg, bar, col, row);
+        tma_load_2d(to + 8 * kBox, &maps.wu, bar, col, row);
+      } else {
+        tma_load_2d(to, &maps.wd, bar, col, row);
+      }
+    }
+  }
+}
+
+// few_up's weights: one lane. Items go round the groups of all blocks.
+template <typename X>
+__device__ bool produce_up_weights(const FewMaps& maps, const FewArgs& a, Ctrl& c, Group& g, const Ring& ring, int first,
+                                   int step, Pos& pos, int& issued) {
+  const Work<X, true> work(a, c.plan.n_act, gridDim.x);
+  const int row_bytes = a.d * (int)sizeof(X);
+  for (int i = first; i < work.total; i += step) {
+    const Item w = work.item(i);
+    const int row = c.plan.expert[w.s] * a.I + w.blk * 8;
+    for (int ch = w.c0; ch < w.c1; ++ch) {
+      if (!mbar_wait(&g.empty[pos.stage], pos.phase ^ 1u, &c.abort, a.status, a.limit_ns)) return false;
+      mbar_arrive_expect_tx(&g.full[pos.stage], weight_bytes<X, true>(ch, row_bytes));
+      load_weights<X, true>(maps, ring.base + (size_t)pos.stage * ring.slot, &g.full[pos.stage], ch, row, row_bytes);
       ++issued;
       pos.next(ring.stages);
     }
@@ -497,116 +566,146 @@ __device__ bool produce_weights(const FewMaps& maps, const FewArgs& a, Ctrl& c, 
   return true;
 }
 
-// The token rows' producer: one warp, lane l copies row l of x, or lane 0 all
-// hidden rows.
-template <typename X, bool kUp>
-__device__ bool produce_tokens(const FewArgs& a, Ctrl& c, const Ring& ring, Pos& pos, int& issued) {
+// few_up's token rows: one warp, lane l copies row l.
+template <typename X>
+__device__ bool produce_up_tokens(const FewArgs& a, Ctrl& c, Group& g, const Ring& ring, int first, int step, Pos& pos,
+                                  int& issued) {
   const int lane = threadIdx.x & 31;
-  const Work<X, kUp> work(a, c.plan);
-  const int row_bytes = (kUp ? a.d : a.I) * (int)sizeof(X);
-  for (int i = blockIdx.x; i < work.total; i += gridDim.x) {
+  const Work<X, true> work(a, c.plan.n_act, gridDim.x);
+  const int row_bytes = a.d * (int)sizeof(X);
+  for (int i = first; i < work.total; i += step) {
     const Item w = work.item(i, c.plan);
     const uint8_t* src = nullptr;
-    if (kUp && lane < w.n)
-      src = static_cast<const uint8_t*>(a.x) + (size_t)(c.plan.tj[w.first + lane] / a.k) * row_bytes;
+    if (lane < w.n) src = static_cast<const uint8_t*>(a.x) + (size_t)(c.plan.tj[w.first + lane] / a.k) * row_bytes;
     for (int ch = w.c0; ch < w.c1; ++ch) {
-      const uint32_t bytes = kUp ? (uint32_t)min(kChunk, row_bytes - ch * kChunk)
-                                 : (uint32_t)(w.n * Traits<X>::kHid * kTokPitch);
+      const uint32_t bytes = (uint32_t)min(kChunk, row_bytes - ch * kChunk);
       bool free = true;
       if (lane == 0) {
-        free = mbar_wait(&c.empty[pos.stage], pos.phase ^ 1u, &c.abort, a.status, a.limit_ns);
-        if (free) mbar_arrive_expect_tx(&c.full[pos.stage], kUp ? w.n * bytes : bytes);
+        free = mbar_wait(&g.empty[pos.stage], pos.phase ^ 1u, &c.abort, a.status, a.limit_ns);
+        if (free) mbar_arrive_expect_tx(&g.full[pos.stage], w.n * bytes);
       }
       if (!__shfl_sync(0xffffffffu, (int)free, 0)) return false;
-      uint8_t* dst = ring.base + (size_t)pos.stage * ring.slot + kWeightBytes;
-      if (kUp) {
-        if (src) bulk_load(dst + lane * kTokPitch, src + (size_t)ch * kChunk, bytes, &c.full[pos.stage]);
-      } else if (lane == 0) {
-        bulk_load(dst, static_cast<const uint8_t*>(a.h) + hidden_at<X>(w.first, w.n, work.chunks, ch, 0), bytes,
-                  &c.full[pos.stage]);
-      }
+      if (src)
+        bulk_load(ring.base + (size_t)pos.stage * ring.slot + kWeightBytes + lane * kTokPitch, src + (size_t)ch * kChunk,
+                  bytes, &g.full[pos.stage]);
       ++issued;
       pos.next(ring.stages);
     }
   }
   return true;
+}
+
+// few_down's weights and hidden rows: one lane. After its first item a group
+// takes the next that nobody has: SMs reach the memory at rates some 10 %
+// apart. The number is asked for an item ahead.
+template <typename X>
+__device__ bool produce_down(const FewMaps& maps, const FewArgs& a, Ctrl& c, Group& g, const Ring& ring, int first,
+                             int step, Pos& pos, int& issued) {
+  const Work<X, false> work(a, c.plan.n_act, gridDim.x);
+  const int row_bytes = a.I * (int)sizeof(X);
+  int i = first;
+  while (true) {
+    const bool more = i < work.total;
+    const int next = more ? step + atomicAdd(a.next, 1) : 0;
+    Item w = {};
+    if (more) w = work.item(i, c.plan);
+    for (int ch = w.c0; ch < (more ? w.c1 : w.c0 + 1); ++ch) {
+      if (!mbar_wait(&g.empty[pos.stage], pos.phase ^ 1u, &c.abort, a.status, a.limit_ns)) return false;
+      g.item[pos.stage] = more ? i : -1;
+      const uint32_t bytes = (uint32_t)(w.n * Traits<X>::kHid * kTokPitch);
+      if (more) {
+        mbar_arrive_expect_tx(&g.full[pos.stage], weight_bytes<X, false>(ch, row_bytes) + bytes);
+        uint8_t* dst = ring.base + (size_t)pos.stage * ring.slot;
+        load_weights<X, false>(maps, dst, &g.full[pos.stage], ch, c.plan.expert[w.s] * a.d + w.blk * kRows, row_bytes);
+        bulk_load(dst + kWeightBytes,
+                  static_cast<const uint8_t*>(a.h) + hidden_at<X>(w.first, w.n, work.chunks, ch, 0), bytes,
+                  &g.full[pos.stage]);
+      } else {
+        mbar_arrive(&g.full[pos.stage]);
+      }
+      ++issued;
+      pos.next(ring.stages);
+    }
+    if (!more) return true;
+    i = next;
+  }
 }
 
 // A block that gives up still waits for the copies it has asked for.
-__device__ void drain(const FewArgs& a, Ctrl& c, const Ring& ring, Pos pos, int issued) {
+__device__ void drain(const FewArgs& a, Group& g, const Ring& ring, Pos pos, int issued) {
   const int n = min(issued, ring.stages);
   for (int i = 0; i < n; ++i) {
     if (pos.stage == 0) pos.stage = ring.stages, pos.phase ^= 1u;
     --pos.stage;
-    if (!mbar_wait(&c.full[pos.stage], pos.phase, nullptr, a.status, a.limit_ns)) return;
+    if (!mbar_wait(&g.full[pos.stage], pos.phase, nullptr, a.status, a.limit_ns)) return;
   }
 }
 
 // Sums of one item into red [parts][kRows][kRedLd]. False: a wait gave up.
 //
-// bf16: warp w takes bytes 256 w .. 256 w + 255 of the stage's rows, 128 at a
-// time. Rows of weights lie 512 bytes apart, so the two rows that a
-// quarter-warp reads at once would fall on the same banks: odd rows take the
-// two halves of the 128 bytes in the other order.
+// bf16: warp w takes bytes 128 w .. 128 w + 127 of the stage's rows. Rows of
+// weights lie 512 bytes apart, so the two rows that a quarter-warp reads at
+// once would fall on the same banks: odd rows take the two halves of the 128
+// bytes in the other order. The halves have sums of their own, which keeps
+// the chains of dependent products short.
 template <bool kUp>
-__device__ bool multiply(const Item& w, const FewArgs& a, Ctrl& c, const Ring& ring, int row_bytes, Pos& pos,
-                         float* red, const __nv_bfloat16*) {
+__device__ bool multiply(const Item& w, const FewArgs& a, Ctrl& c, Group& g, const Ring& ring, int warp, int row_bytes,
+                         Pos& pos, float* red, const __nv_bfloat16*) {
   constexpr int kTiles = kUp ? 2 : 4;  // of 8 columns: a token each, or hi and lo of four
-  const int warp = (threadIdx.x >> 5) - 2, lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31;
   const int r = lane >> 2, q = lane & 3;
   const bool odd = r & 1;
   const int cols = kUp ? w.n : 2 * w.n;
-  float acc[kTiles][4];
+  float acc[2][kTiles][4];
 #pragma unroll
   for (int j = 0; j < kTiles; ++j)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
+    for (int i = 0; i < 4; ++i) acc[0][j][i] = acc[1][j][i] = 0.f;
   const uint4 zero = make_uint4(0, 0, 0, 0);
+  const int wo = (warp >> 2) * kRows * kBox + (warp & 3) * 128 + r * kBox + q * 16;
+  const int to = kWeightBytes + warp * 128 + q * 16;
   for (int ch = w.c0; ch < w.c1; ++ch) {
-    if (!__all_sync(0xffffffffu, mbar_wait(&c.full[pos.stage], pos.phase, &c.abort, a.status, a.limit_ns))) return false;
+    if (!__all_sync(0xffffffffu, mbar_wait(&g.full[pos.stage], pos.phase, &c.abort, a.status, a.limit_ns))) return false;
     const uint8_t* slot = ring.base + (size_t)pos.stage * ring.slot;
-    const int have = row_bytes - ch * kChunk;
-    const uint8_t* pw = slot + (warp >> 1) * kRows * kBox + (warp & 1) * 256 + r * kBox + q * 16;
-    const uint8_t* pt = slot + kWeightBytes + warp * 256 + q * 16;
+    const int have = row_bytes - ch * kChunk, off = warp * 128;
+    if (off < have) {
+      const uint8_t* pw = slot + wo;
+      const uint4 l0 = *reinterpret_cast<const uint4*>(pw + (odd ? 64 : 0));
+      const uint4 l1 = *reinterpret_cast<const uint4*>(pw + (odd ? 0 : 64));
+      const uint4 h0 = *reinterpret_cast<const uint4*>(pw + 8 * kBox + (odd ? 64 : 0));
+      const uint4 h1 = *reinterpret_cast<const uint4*>(pw + 8 * kBox + (odd ? 0 : 64));
+      const uint4 a0 = odd ? l1 : l0, a1 = odd ? l0 : l1;
+      const uint4 b0 = odd ? h1 : h0, b1 = odd ? h0 : h1;
+      // the weights end in zeros; the token rows in what was there before
+      const bool in0 = off + q * 16 < have, in1 = off + 64 + q * 16 < have;
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int off = warp * 256 + u * 128;
-      if (off < have) {
-        uint4 lo[2], hi[2];
-        lo[0] = *reinterpret_cast<const uint4*>(pw + u * 128 + (odd ? 64 : 0));
-        lo[1] = *reinterpret_cast<const uint4*>(pw + u * 128 + (odd ? 0 : 64));
-        hi[0] = *reinterpret_cast<const uint4*>(pw + u * 128 + 8 * kBox + (odd ? 64 : 0));
-        hi[1] = *reinterpret_cast<const uint4*>(pw + u * 128 + 8 * kBox + (odd ? 0 : 64));
-        const uint4 a0 = odd ? lo[1] : lo[0], a1 = odd ? lo[0] : lo[1];
-        const uint4 b0 = odd ? hi[1] : hi[0], b1 = odd ? hi[0] : hi[1];
-        // the weights end in zeros; the token rows in what was there before
-        const bool in0 = off + q * 16 < have, in1 = off + 64 + q * 16 < have;
-#pragma unroll
-        for (int j = 0; j < kTiles; ++j) {
-          if (j * 8 < cols) {
-            const uint8_t* p = pt + u * 128 + min(j * 8 + r, cols - 1) * kTokPitch;
-            const uint4 t0 = in0 ? *reinterpret_cast<const uint4*>(p) : zero;
-            const uint4 t1 = in1 ? *reinterpret_cast<const uint4*>(p + 64) : zero;
-            mma_block(acc[j], a0, b0, t0);
-            mma_block(acc[j], a1, b1, t1);
-          }
+      for (int j = 0; j < kTiles; ++j) {
+        if (j * 8 < cols) {
+          const uint8_t* p = slot + to + min(j * 8 + r, cols - 1) * kTokPitch;
+          const uint4 t0 = in0 ? *reinterpret_cast<const uint4*>(p) : zero;
+          const uint4 t1 = in1 ? *reinterpret_cast<const uint4*>(p + 64) : zero;
+          mma_block(acc[0][j], a0, b0, t0);
+          mma_block(acc[1][j], a1, b1, t1);
         }
       }
     }
     __syncwarp();
-    if (lane == 0) mbar_arrive(&c.empty[pos.stage]);
+    if (lane == 0) mbar_arrive(&g.empty[pos.stage]);
     pos.next(ring.stages);
   }
   float* mine = red + warp * kRows * kRedLd;
 #pragma unroll
   for (int j = 0; j < kTiles; ++j) {
     if (j * 8 < cols) {
+      float s[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[i] = acc[0][j][i] + acc[1][j][i];
       if (kUp) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) mine[(r + (i >> 1) * 8) * kRedLd + j * 8 + q * 2 + (i & 1)] = acc[j][i];
+        for (int i = 0; i < 4; ++i) mine[(r + (i >> 1) * 8) * kRedLd + j * 8 + q * 2 + (i & 1)] = s[i];
       } else {  // columns 2t and 2t + 1: the two terms of token t
-        mine[r * kRedLd + j * 4 + q] = acc[j][0] + acc[j][1];
-        mine[(r + 8) * kRedLd + j * 4 + q] = acc[j][2] + acc[j][3];
+        mine[r * kRedLd + j * 4 + q] = s[0] + s[1];
+        mine[(r + 8) * kRedLd + j * 4 + q] = s[2] + s[3];
       }
     }
   }
@@ -615,53 +714,49 @@ __device__ bool multiply(const Item& w, const FewArgs& a, Ctrl& c, const Ring& r
 
 // fp32: warp w takes rows 4 (w / 2) .. + 3 and half of the stage's columns.
 template <bool kUp>
-__device__ bool multiply(const Item& w, const FewArgs& a, Ctrl& c, const Ring& ring, int row_bytes, Pos& pos,
-                         float* red, const float*) {
-  const int warp = (threadIdx.x >> 5) - 2, lane = threadIdx.x & 31;
+__device__ bool multiply(const Item& w, const FewArgs& a, Ctrl& c, Group& g, const Ring& ring, int warp, int row_bytes,
+                         Pos& pos, float* red, const float*) {
+  const int lane = threadIdx.x & 31;
   const int half = warp & 1, r0 = (warp >> 1) * 4;
   float acc[4][16];  // [four tokens][row * 4 + token]
 #pragma unroll
-  for (int g = 0; g < 4; ++g)
+  for (int q = 0; q < 4; ++q)
 #pragma unroll
-    for (int i = 0; i < 16; ++i) acc[g][i] = 0.f;
+    for (int i = 0; i < 16; ++i) acc[q][i] = 0.f;
   for (int ch = w.c0; ch < w.c1; ++ch) {
-    if (!__all_sync(0xffffffffu, mbar_wait(&c.full[pos.stage], pos.phase, &c.abort, a.status, a.limit_ns))) return false;
+    if (!__all_sync(0xffffffffu, mbar_wait(&g.full[pos.stage], pos.phase, &c.abort, a.status, a.limit_ns))) return false;
     const uint8_t* slot = ring.base + (size_t)pos.stage * ring.slot;
-    const int have = row_bytes - ch * kChunk;
+    const int off = half * kBox + lane * 16;
+    if (off < row_bytes - ch * kChunk) {
+      const uint8_t* pw = slot + half * kRows * kBox + r0 * kBox + lane * 16;
+      const uint8_t* pt = slot + kWeightBytes + off;
+      float4 wv[4];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int box = half * 2 + u, off = box * kBox + lane * 16;
-      if (off < have) {
-        const uint8_t* pw = slot + box * kRows * kBox + r0 * kBox + lane * 16;
-        const uint8_t* pt = slot + kWeightBytes + off;
-        float4 wv[4];
+      for (int i = 0; i < 4; ++i) wv[i] = *reinterpret_cast<const float4*>(pw + i * kBox);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) wv[i] = *reinterpret_cast<const float4*>(pw + i * kBox);
+      for (int q = 0; q < 4; ++q) {
+        if (q * 4 < w.n) {
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          if (g * 4 < w.n) {
+          for (int t = 0; t < 4; ++t) {
+            const float4 b = *reinterpret_cast<const float4*>(pt + (q * 4 + t) * kTokPitch);
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-              const float4 b = *reinterpret_cast<const float4*>(pt + (g * 4 + t) * kTokPitch);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                float& s = acc[g][i * 4 + t];
-                s = fmaf(wv[i].w, b.w, fmaf(wv[i].z, b.z, fmaf(wv[i].y, b.y, fmaf(wv[i].x, b.x, s))));
-              }
+            for (int i = 0; i < 4; ++i) {
+              float& s = acc[q][i * 4 + t];
+              s = fmaf(wv[i].w, b.w, fmaf(wv[i].z, b.z, fmaf(wv[i].y, b.y, fmaf(wv[i].x, b.x, s))));
             }
           }
         }
       }
     }
     __syncwarp();
-    if (lane == 0) mbar_arrive(&c.empty[pos.stage]);
+    if (lane == 0) mbar_arrive(&g.empty[pos.stage]);
     pos.next(ring.stages);
   }
 #pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    if (g * 4 < w.n) {
-      const float s = reduce_many(acc[g]);
-      if ((lane & 1) == 0) red[(half * kRows + r0 + (lane >> 3)) * kRedLd + g * 4 + ((lane >> 1) & 3)] = s;
+  for (int q = 0; q < 4; ++q) {
+    if (q * 4 < w.n) {
+      const float s = reduce_many(acc[q]);
+      if ((lane & 1) == 0) red[(half * kRows + r0 + (lane >> 3)) * kRedLd + q * 4 + ((lane >> 1) & 3)] = s;
     }
   }
   return true;
@@ -687,78 +782,145 @@ __device__ __forceinline__ float sum_parts(const float* red, int row, int n) {
   return s;
 }
 
-template <typename X, bool kUp>
-__device__ void consume(const FewArgs& a, Ctrl& c, const Ring& ring, float* red2) {
-  const Work<X, kUp> work(a, c.plan);
+// few_up's products.
+template <typename X>
+__device__ void consume_up(const FewArgs& a, Ctrl& c, Group& g, const Ring& ring, float* red2, int group, int first,
+                           int step) {
+  const Work<X, true> work(a, c.plan.n_act, gridDim.x);
   const int hid_chunks = (a.I * (int)sizeof(X) + kChunk - 1) / kChunk;
-  const int K = kUp ? a.d : a.I;
-  const int tid = threadIdx.x - 64;
-  const int R = a.T * a.k;
+  const int tid = threadIdx.x - (group * kGroupWarps + 2) * 32;
   Pos pos;
   int buf = 0;
-  for (int i = blockIdx.x; i < work.total; i += gridDim.x) {
+  for (int i = first; i < work.total; i += step) {
     const Item w = work.item(i, c.plan);
     float* red = red2 + buf * red_floats<X>();
     buf ^= 1;
-    const bool ok = multiply<kUp>(w, a, c, ring, K * (int)sizeof(X), pos, red, static_cast<const X*>(nullptr));
-    if (!math_sync_all(ok)) break;
-    if (kUp) {
-      const int u = tid & 7, n = tid >> 3, unit = w.blk * 8 + u;
-      if (n < w.n && unit < a.I) {
-        const float g = sum_parts<X>(red, u, n), up = sum_parts<X>(red, 8 + u, n);
-        const int ch = unit * (int)sizeof(X) / kChunk, at = unit * (int)sizeof(X) % kChunk;
-        put_hidden(static_cast<uint8_t*>(a.h) + hidden_at<X>(w.first, w.n, hid_chunks, ch, n * Traits<X>::kHid) + at,
-                   silu_of(g, static_cast<const X*>(nullptr)) * up, static_cast<const X*>(nullptr));
-      }
-    } else {
+    const bool ok =
+        multiply<true>(w, a, c, g, ring, tid >> 5, a.d * (int)sizeof(X), pos, red, static_cast<const X*>(nullptr));
+    if (!math_sync_all(group, ok)) return;
+    const int u = tid & 7, n = tid >> 3, unit = w.blk * 8 + u;
+    if (n < w.n && unit < a.I) {
+      const float gt = sum_parts<X>(red, u, n), up = sum_parts<X>(red, 8 + u, n);
+      const int ch = unit * (int)sizeof(X) / kChunk, at = unit * (int)sizeof(X) % kChunk;
+      put_hidden(static_cast<uint8_t*>(a.h) + hidden_at<X>(w.first, w.n, hid_chunks, ch, n * Traits<X>::kHid) + at,
+                 silu_of(gt, static_cast<const X*>(nullptr)) * up, static_cast<const X*>(nullptr));
+    }
+  }
+}
+
+// A group's parts since its last join are counted, and the blocks of columns
+// whose last part that was are added up: part by part of the columns, over a
+// token's experts in slot order.
+// Once for many items: the fence and the atomic's round trip after every item
+// took as long as its product.
+template <typename X>
+__device__ void join(const FewArgs& a, Ctrl& c, Group& g, const Work<X, false>& work, int group, int tid, int n) {
+  const int R = a.T * a.k, all = c.plan.n_act * work.split;
+  __threadfence();
+  if (tid == 0) g.n_last = 0;
+  math_sync(group);
+  if (tid < n) {
+    const int blk = g.blk[tid];
+    if (atomicAdd(&a.done[blk], 1) == all - 1) g.last[atomicAdd(&g.n_last, 1)] = blk;
+  }
+  math_sync(group);
+  __threadfence();
+  for (int u = tid; u < g.n_last * a.T * kRows; u += kMath) {
+    const int r = u % kRows, q = u / kRows, t = q % a.T, col = g.last[q / a.T] * kRows + r;
+    if (col >= a.d) continue;
+    const float* y = a.y + (size_t)t * a.k * a.d + col;
+    float s = 0.f;
+    for (int p = 0; p < work.split; ++p) {
+#pragma unroll 4
+      for (int j = 0; j < a.k; ++j) s += __ldcg(y + ((size_t)p * R + j) * a.d);
+    }
+    put(static_cast<X*>(a.out) + (size_t)t * a.d + col, s);
+  }
+  math_sync(group);
+}
+
+// few_down's products.
+template <typename X>
+__device__ void consume_down(const FewArgs& a, Ctrl& c, Group& g, const Ring& ring, float* red2, int group) {
+  const Work<X, false> work(a, c.plan.n_act, gridDim.x);
+  const int tid = threadIdx.x - (group * kGroupWarps + 2) * 32;
+  const int R = a.T * a.k;
+  Pos pos;
+  int buf = 0, n_blk = 0;
+  while (true) {
+    // the stage says which item begins
+    bool ok = __all_sync(0xffffffffu, mbar_wait(&g.full[pos.stage], pos.phase, &c.abort, a.status, a.limit_ns));
+    const int i = ok ? g.item[pos.stage] : -1;
+    if (i >= 0) {
+      const Item w = work.item(i, c.plan);
+      float* red = red2 + buf * red_floats<X>();
+      buf ^= 1;
+      ok = multiply<false>(w, a, c, g, ring, tid >> 5, a.I * (int)sizeof(X), pos, red, static_cast<const X*>(nullptr));
+      if (tid == 0) g.blk[n_blk] = w.blk;
+      if (!math_sync_all(group, ok)) return;
       const int r = tid & 15, n = tid >> 4, col = w.blk * kRows + r;
       if (n < w.n && col < a.d)
-        a.y[((size_t)w.part * R + c.plan.tj[w.first + n]) * a.d + col] = c.plan.gate[w.first + n] * sum_parts<X>(red, r, n);
-      __threadfence();
-      math_sync();
-      if (tid == 0) {
-        const int before = atomicAdd(&a.done[w.blk], 1);
-        c.last = before == c.plan.n_act * work.split - 1;
+        a.y[((size_t)w.part * R + c.plan.tj[w.first + n]) * a.d + col] =
+            c.plan.gate[w.first + n] * sum_parts<X>(red, r, n);
+      if (++n_blk == kMath) {
+        join<X>(a, c, g, work, group, tid, n_blk);
+        n_blk = 0;
       }
-      math_sync();
-      if (c.last) {
-        __threadfence();
-        if (n < a.T && col < a.d) {
-          float s = 0.f;
-          for (int j = 0; j < a.k; ++j)
-            for (int q = 0; q < work.split; ++q) s += __ldcg(&a.y[((size_t)q * R + n * a.k + j) * a.d + col]);
-          put(static_cast<X*>(a.out) + (size_t)n * a.d + col, s);
-        }
-      }
+    } else {
+      if (!math_sync_all(group, ok)) return;
+      if (n_blk) join<X>(a, c, g, work, group, tid, n_blk);
+      return;
     }
   }
 }
 
 template <typename X, bool kUp>
 __device__ void stream(const FewMaps& maps, const FewArgs& a, Ctrl& c, uint8_t* smem_ring, float* red) {
-  const Ring ring = ring_of<X, kUp>(smem_ring, c.plan);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31;
+  const int group = (int)(threadIdx.x >> 5) / kGroupWarps, role = (int)(threadIdx.x >> 5) % kGroupWarps;
+  const Ring ring = ring_of<X, kUp>(smem_ring, c.plan, group);
+  if (group >= ring.groups) return;
+  Group& g = c.group[group];
+  const int first = blockIdx.x * ring.groups + group, step = gridDim.x * ring.groups;
   Pos pos;
   int issued = 0;
-  if (warp == 0) {
-    if (lane == 0 && (!produce_weights<X, kUp>(maps, a, c, ring, pos, issued) || c.abort))
-      drain(a, c, ring, pos, issued);
+  if (role == 0) {
+    if (lane == 0) {
+      bool ok;
+      if constexpr (kUp)
+        ok = produce_up_weights<X>(maps, a, c, g, ring, first, step, pos, issued);
+      else
+        ok = produce_down<X>(maps, a, c, g, ring, first, step, pos, issued);
+      // few_down's first stages, while this kernel ends and that one starts
+      if (kUp && ok && group == 0)
+        for (int b = blockIdx.x; b < a.down_blocks; b += gridDim.x)
+          prefetch_weights<X, false>(maps, a, c.plan.expert, c.plan.n_act, b, a.down_blocks);
+      if (!ok || c.abort) drain(a, g, ring, pos, issued);
+    }
     __syncwarp();
-  } else if (warp == 1) {
-    const bool ok = produce_tokens<X, kUp>(a, c, ring, pos, issued);
-    if (lane == 0 && (!ok || c.abort)) drain(a, c, ring, pos, issued);
-    __syncwarp();
+  } else if (role == 1) {
+    if constexpr (kUp) {
+      const bool ok = produce_up_tokens<X>(a, c, g, ring, first, step, pos, issued);
+      if (lane == 0 && (!ok || c.abort)) drain(a, g, ring, pos, issued);
+      __syncwarp();
+    }
   } else {
-    consume<X, kUp>(a, c, ring, red);
+    red += group * 2 * red_floats<X>();
+    if constexpr (kUp)
+      consume_up<X>(a, c, g, ring, red, group, first, step);
+    else
+      consume_down<X>(a, c, g, ring, red, group);
   }
 }
 
+template <typename X, bool kUp>
 __device__ __forceinline__ void init_ctrl(Ctrl& c) {
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kMaxStages; ++s) {
-      mbar_init(&c.full[s], 2);
-      mbar_init(&c.empty[s], kMathWarps);
-    }
+    for (int q = 0; q < Traits<X>::kGroups; ++q)
+      for (int s = 0; s < kMaxStages; ++s) {
+        mbar_init(&c.group[q].full[s], kUp ? 2 : 1);  // few_up has two producers
+        mbar_init(&c.group[q].empty[s], kMathWarps);
+      }
     c.abort = 0;
     fence_mbarrier_init();
   }
@@ -768,49 +930,53 @@ template <typename X>
 __device__ __forceinline__ void carve(uint8_t* smem, Ctrl** c, float** red, uint8_t** ring) {
   *c = reinterpret_cast<Ctrl*>(smem);
   *red = reinterpret_cast<float*>(smem + (sizeof(Ctrl) + 127) / 128 * 128);
-  *ring = reinterpret_cast<uint8_t*>(*red + 2 * red_floats<X>());
+  *ring = reinterpret_cast<uint8_t*>(*red + 2 * Traits<X>::kGroups * red_floats<X>());
 }
 
 template <typename X>
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1) few_up_kernel(const __grid_constant__ FewMaps maps, const FewArgs a) {
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(threads<X>(), 1) few_up_kernel(const __grid_constant__ FewMaps maps, const FewArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
   Ctrl* c;
   float* red;
   uint8_t* ring;
   carve<X>(smem, &c, &red, &ring);
-  init_ctrl(*c);
+  init_ctrl<X, true>(*c);
+  if (a.likely && threadIdx.x == 32) prefetch_weights<X, true>(maps, a, nullptr, a.E, blockIdx.x, gridDim.x);
   float* part = reinterpret_cast<float*>(ring);                     // [kCluster][T][E]
-  float* scratch = part + (size_t)kCluster * a.T * a.E;             // [kWarps][kPassE][16]
+  float* scratch = part + (size_t)kCluster * a.T * a.E;             // [kWarps][16][kPassLd]
   const int rank = (int)cluster_ctarank();
   cluster_sync();  // the peers' shared memory exists
   pdl_wait();
   pdl_trigger();
+  if (blockIdx.x == 0) {  // few_down counts on zeros
+    for (int i = threadIdx.x; i < (a.d + kRows - 1) / kRows; i += blockDim.x) a.done[i] = 0;
+    if (threadIdx.x == 0) *a.next = 0;
+  }
+  for (int e = threadIdx.x; e < a.E; e += blockDim.x) c->bias[e] = a.br ? a.br[e] : 0.f;
   // this CTA's columns
   const int unit = 32, units = (a.d + unit - 1) / unit;
   const int c0 = min(a.d, rank * units / kCluster * unit), c1 = min(a.d, (rank + 1) * units / kCluster * unit);
-  logits_part(static_cast<const X*>(a.x), static_cast<const X*>(a.wr), a.T, a.d, a.E, c0, c1, scratch, part, rank);
+  logits_part(static_cast<const X*>(a.x), static_cast<const X*>(a.wr), a.T, a.d, a.E, c0, c1, c->bias, scratch,
+              part, rank);
   cluster_sync();  // all parts are here, and no peer writes here any more
   const bool first = blockIdx.x == 0;
-  choose<X>(a, part, *c, first);
+  choose(a, part, *c, first);
   __syncthreads();
   make_plan(c->plan, c->idx, c->gate, a.T, a.E, a.k);
-  if (first) {
-    statistics(a, part, *c);
-    for (int i = threadIdx.x; i < (a.d + kRows - 1) / kRows; i += kThreads) a.done[i] = 0;
-  }
+  if (first && (a.counts || a.aux)) statistics(a, part, *c);
   fence_async();  // the ring's memory was written above, and is next by the copies
   __syncthreads();
   stream<X, true>(maps, a, *c, ring, red);
 }
 
 template <typename X>
-__global__ void __launch_bounds__(kThreads, 1) few_down_kernel(const __grid_constant__ FewMaps maps, const FewArgs a) {
+__global__ void __launch_bounds__(threads<X>(), 1) few_down_kernel(const __grid_constant__ FewMaps maps, const FewArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
   Ctrl* c;
   float* red;
   uint8_t* ring;
   carve<X>(smem, &c, &red, &ring);
-  init_ctrl(*c);
+  init_ctrl<X, false>(*c);
   pdl_wait();
   pdl_trigger();
   const int i = threadIdx.x;
@@ -855,7 +1021,7 @@ cudaError_t device_info(Device* out) {
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(kCluster, 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.blockDim = dim3(threads<X>(), 1, 1);
   cfg.dynamicSmemBytes = kSmemTotal;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
@@ -872,17 +1038,24 @@ cudaError_t device_info(Device* out) {
 }
 
 template <typename X>
-cudaError_t launch(const FewMaps& m, const FewArgs& a, cudaStream_t stream) {
-  // the routing's scratch lies where the ring is, and every ring has two stages
+cudaError_t launch(const FewMaps& m, FewArgs a, cudaStream_t stream) {
+  // the routing's scratch lies where the rings are, and a single group's has at least three stages
   constexpr int kRing = kSmemTotal - fixed_bytes<X>();
-  static_assert(4 * (kCluster * kFewTokens * kMaxExperts + kWarps * kPassE * kFewTokens) <= kRing, "routing scratch");
-  static_assert(2 * (kWeightBytes + Traits<X>::kHid * kFewTokens * kTokPitch + 128) <= kRing, "ring");
+  static_assert(4 * (kCluster * kFewTokens * kMaxExperts + threads<X>() / 32 * kFewTokens * kPassLd) <= kRing, "routing scratch");
+  static_assert(3 * (kWeightBytes + Traits<X>::kHid * kFewTokens * kTokPitch + 128) <= kRing, "ring");
   Device dev;
   cudaError_t err = device_info<X>(&dev);
   if (err != cudaSuccess) return err;
-  err = launch_pdl(few_up_kernel<X>, dim3(dev.clusters * kCluster), dim3(kThreads), kSmemTotal, stream, m, a);
+  a.down_blocks = dev.sms;
+  // an expert is left out with probability (1 - k / E)^T if they are drawn
+  // evenly: where that is rare, all experts' first weights are asked for
+  // before the routing is known
+  double out = 1.0;
+  for (int t = 0; t < a.T; ++t) out *= 1.0 - (double)a.k / a.E;
+  a.likely = out < 0.05;
+  err = launch_pdl(few_up_kernel<X>, dim3(dev.clusters * kCluster), dim3(threads<X>()), kSmemTotal, stream, m, a);
   if (err != cudaSuccess) return err;
-  return launch_pdl(few_down_kernel<X>, dim3(dev.sms), dim3(kThreads), kSmemTotal, stream, m, a);
+  return launch_pdl(few_down_kernel<X>, dim3(dev.sms), dim3(threads<X>()), kSmemTotal, stream, m, a);
 }
 
 }  // namespace
@@ -894,6 +1067,7 @@ FewWorkspace few_layout(int T, int d, int k, int I, moe_dtype dtype) {
   // of 16 columns do not go evenly into the SMs
   w.split = R > 0 && 256 / R < kFewMaxSplit ? (int)(256 / R) : kFewMaxSplit;
   size_t o = 0;
+  w.next = o; o = align256(o + 4);
   w.done = o; o = align256(o + 4 * (size_t)((d + kRows - 1) / kRows));
   const size_t chunks = (el * (size_t)I + kChunk - 1) / kChunk;
   w.h = o;    o = align256(o + R * chunks * kTokPitch * (dtype == MOE_BF16 ? Traits<__nv_bfloat16>::kHid : 1));

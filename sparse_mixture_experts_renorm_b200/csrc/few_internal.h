@@ -8,10 +8,11 @@ namespace moe {
 
 constexpr int kFewTokens = MOE_FEW_TOKENS;  // two n8 tiles of an mma.sync step
 constexpr int kFewMaxSplit = 8;                // parts of a down product's columns
-constexpr int kFewTokPitch = 2048 + 64;        // bytes between token rows in shared memory and of hidden rows
+constexpr int kFewTokPitch = 1024 + 64;        // bytes between token rows in shared memory and of hidden rows
 
 // Byte offsets inside the workspace.
 struct FewWorkspace {
+  size_t next;   // int32 [1] few_down's next item
   size_t done;   // int32 [blocks of 16 output columns] finished parts
   size_t h;      // hidden rows by expert and chunk of columns (few.cu, hidden_at)
   size_t y;      // fp32  [split, T*k, d] gated expert outputs
@@ -28,10 +29,13 @@ struct FewArgs {
   float* gate;
   int32_t* counts;  // NULL: not wanted
   float* aux;       // NULL: not wanted
+  int32_t* next;
   int32_t* done;
   void* h;
   float* y;
   int split;        // parts that y has room for
+  int down_blocks;  // few_down's grid, set by the launcher
+  int likely;       // nearly every expert will get tokens, set by the launcher
   int32_t* status;
   uint64_t limit_ns;
 };
