@@ -34,7 +34,7 @@ namespace {
 
 constexpr int kMathWarps = 8;
 constexpr int kMath = 32 * kMathWarps;
-constexpr int kGroupWarps = 2 + kMathWarps;  // a group: 0: weights, 1: token rows, 2..9: products
+constexpr int kGroupWarps = 2 + kMathWarps;  // a group: 0: weights, 1: token rows or joins, 2..9: products
 constexpr int kMaxGroups = 2;
 constexpr int kRows = 16;                // weight rows of a stage
 constexpr int kBox = 512;                // bytes of a row in one tile load
@@ -44,7 +44,8 @@ constexpr int kWeightBytes = kRows * kChunk;
 constexpr int kTokPitch = kFewTokPitch;  // bytes between token rows: two rows of a quarter-warp's load on different banks
 static_assert(kTokPitch == kChunk + 64, "pitch");
 constexpr int kMaxStages = 10;           // of a group
-constexpr int kAhead = 16;               // stages of a block brought to L2 ahead of time: 38 MB on 148 SMs
+constexpr int kAhead = 8;                // stages of a block brought to L2 ahead of time: 19 MB on 148 SMs
+constexpr int kJoinQueue = 256;          // items that the joins may lie behind the products
 constexpr int kMaxRows = kFewTokens * kMaxTopK;
 constexpr int kCluster = 4;              // CTAs that share one routing
 constexpr int kPassE = 64;               // experts whose logits a warp holds at a time
@@ -67,9 +68,9 @@ struct Group {
   uint64_t full[kMaxStages];   // the producers' bytes
   uint64_t empty[kMaxStages];  // the math warps
   int item[kMaxStages];        // few_down: the item that a stage begins, or -1: there are no more
-  int n_last;
-  int blk[kMath];              // few_down: blocks of output columns of the items since the last join
-  int last[kMath];             // and those of them to add up
+  int blk[kJoinQueue];         // few_down: block of output columns of each finished item
+  volatile int finished;       // items whose parts are written; negative: ~items, and there are no more
+  volatile int joined;         // items that have been counted
 };
 
 struct Ctrl {
@@ -142,10 +143,8 @@ __device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int x, i
                : "memory");
 }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
-__device__ __forceinline__ void math_sync(int group) {
-  asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(kMath) : "memory");
-}
-// The same, and whether any thread of it said no: all leave together.
+// A barrier of a group's math warps, and whether any thread said no: all
+// leave together.
 __device__ __forceinline__ bool math_sync_all(int group, bool ok) {
   uint32_t any;
   asm volatile(
@@ -341,60 +340,63 @@ __device__ __forceinline__ float key_value(uint32_t key) {
   return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
 }
 
-// Softmax, the k best (ties to the lower index) and their gates, one warp a
-// token. part [kCluster][T][E]; the logits replace part[0], and then the
-// probabilities if the statistic is wanted. The loops stay rolled: the code
-// runs once, and fetching it is what it would wait for.
-__device__ void choose(const FewArgs& a, float* part, Ctrl& c, bool write) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int T = a.T, E = a.E, k = a.k;
-  for (int t = warp; t < T; t += blockDim.x / 32) {
-    float* row = part + (size_t)t * E;
-    bool finite = true;
-    uint32_t best = 0;
-#pragma unroll 1
-    for (int e = lane; e < E; e += 32) {
+// Softmax, the k best (ties to the lower index) and their gates. part
+// [kCluster][T][E]; the logits replace part[0], and then the probabilities if
+// the statistic is wanted. An expert's place is the number of those before it
+// in its token's row, counted by a thread per (token, expert): k rounds of an
+// arg-max by a warp per token took 2.0 us for 64 experts and k = 6, this 0.6.
+// Experts rank by their logits, as their exact probabilities do; NaN ranks
+// lowest, so that every token still gets k different experts. keys [T][E
+// rounded to 4].
+__device__ void choose(const FewArgs& a, float* part, uint32_t* keys, Ctrl& c, bool write) {
+  const int T = a.T, E = a.E, k = a.k, ld = (E + 3) & ~3;
+  for (int i = threadIdx.x; i < T * ld; i += blockDim.x) {
+    const int t = i / ld, e = i - t * ld;
+    uint32_t key = 0;
+    if (e < E) {
       float s = 0.f;
 #pragma unroll
-      for (int q = 0; q < kCluster; ++q) s += row[(size_t)q * T * E + e];
-      finite = finite && isfinite(s);
-      row[e] = s;
-      best = max(best, rank_key(s));
+      for (int q = 0; q < kCluster; ++q) s += part[((size_t)q * T + t) * E + e];
+      part[(size_t)t * E + e] = s;
+      if (write && !isfinite(s)) atomicOr(a.status, MOE_DEV_NONFINITE);
+      key = rank_key(s);
     }
-    const float m = key_value(__reduce_max_sync(0xffffffffu, best));
+    keys[i] = key;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < T * E; i += blockDim.x) {
+    const int t = i / E, e = i - t * E;
+    const uint32_t mine = keys[t * ld + e];
+    const uint4* row = reinterpret_cast<const uint4*>(keys + t * ld);
+    int place = 0;
+    for (int j = 0; j < ld; j += 4) {
+      const uint4 v = row[j >> 2];
+      place += (v.x > mine) + (v.y > mine) + (v.z > mine) + (v.w > mine);
+      place += (v.x == mine && j < e) + (v.y == mine && j + 1 < e) + (v.z == mine && j + 2 < e) +
+               (v.w == mine && j + 3 < e);
+    }
+    if (place < k) c.idx[t * k + place] = e;
+  }
+  __syncthreads();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int t = warp; t < T; t += blockDim.x / 32) {
+    float* row = part + (size_t)t * E;
+    const int mine = lane < k ? c.idx[t * k + lane] : 0;
+    const float l = key_value(keys[t * ld + mine]);
+    const float m = __shfl_sync(0xffffffffu, l, 0);
     float sum = 0.f;
-#pragma unroll 1
-    for (int e = lane; e < E; e += 32) sum += expf(row[e] - m);
+    if (!a.renorm || (write && a.aux)) {
+      for (int e = lane; e < E; e += 32) sum += expf(row[e] - m);
 #pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (write && !__all_sync(0xffffffffu, finite) && lane == 0) atomicOr(a.status, MOE_DEV_NONFINITE);
-    // k rounds of an arg-max over the logits, which rank as their exact
-    // probabilities do; NaN ranks lowest, so that every token still gets k
-    // different experts
-    uint32_t taken = 0;
-    float l = -INFINITY;
-    int mine = 0;
-#pragma unroll 1
-    for (int j = 0; j < k; ++j) {
-      best = 0;
-      int be = 0x7fffffff;
-#pragma unroll 1
-      for (int e = lane, i = 0; e < E; e += 32, ++i) {
-        const uint32_t key = (taken >> i) & 1u ? 0u : rank_key(row[e]);
-        if (key > best) best = key, be = e;
-      }
-      const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-      const int e = __reduce_min_sync(0xffffffffu, best == top ? be : 0x7fffffff);
-      if ((e & 31) == lane) taken |= 1u << (e >> 5);
-      if (lane == j) l = key_value(top), mine = e;
+      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     }
-    const float p = expf(l - m) / sum;
-    float total = lane < k ? p : 0.f;
+    // renormalised, the softmax's own sum cancels
+    const float p = lane < k ? expf(l - m) : 0.f;
+    float total = p;
 #pragma unroll
     for (int o = 4; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     if (lane < k) {
-      const float g = !a.renorm ? p : total > 0.f ? p / total : 1.f / (float)k;
-      c.idx[t * k + lane] = mine;
+      const float g = !a.renorm ? p / sum : total > 0.f ? p / total : 1.f / (float)k;
       c.gate[t * k + lane] = g;
       if (write) {
         a.idx[(size_t)t * k + lane] = mine;
@@ -443,18 +445,19 @@ struct Item {
 template <typename X, bool kUp>
 struct Work {
   int n_blk, split, chunks, total;
-  __device__ Work(const FewArgs& a, int n_act, int grid) {
+  // units: groups of all blocks
+  __device__ Work(const FewArgs& a, int n_act, int units) {
     const int K = kUp ? a.d : a.I;
     chunks = (K * (int)sizeof(X) + kChunk - 1) / kChunk;
     n_blk = kUp ? (a.I + 7) / 8 : (a.d + 15) / 16;
     split = 1;
     const int items = n_act * n_blk;
     if (!kUp) {
-      // the parts that leave the busiest block the fewest chunks; a finer
-      // split has to gain 3 %
-      float best = (float)((items + grid - 1) / grid) * (float)chunks;
-      for (int q = 2; q <= min(a.split, chunks); ++q) {
-        const float t = (float)((items * q + grid - 1) / grid) * (float)((chunks + q - 1) / q);
+      // the parts that leave the busiest group the least to do; an item's own
+      // overhead (its sums, its join) is some two chunks
+      float best = 3.0e38f;
+      for (int q = 1; q <= min(a.split, chunks); ++q) {
+        const float t = (float)((items * q + units - 1) / units) * (float)((chunks + q - 1) / q + 2);
         if (t < 0.97f * best) best = t, split = q;
       }
     }
@@ -499,8 +502,8 @@ __device__ __forceinline__ size_t hidden_at(int first, int n, int chunks, int ch
 // Asks for the weights of block `block`'s first stages to be brought to L2.
 template <typename X, bool kUp>
 __device__ void prefetch_weights(const FewMaps& maps, const FewArgs& a, const int* expert, int n_act, int block,
-                                 int grid) {
-  const Work<X, kUp> work(a, n_act, grid);
+                                 int grid, int units) {
+  const Work<X, kUp> work(a, n_act, units);
   const int row_bytes = (kUp ? a.d : a.I) * (int)sizeof(X);
   int n = 0;
   for (int i = block; i < work.total; i += grid) {
@@ -550,7 +553,7 @@ __device__ __forceinline__ void load_weights(const FewMaps& maps, uint8_t* dst, 
 template <typename X>
 __device__ bool produce_up_weights(const FewMaps& maps, const FewArgs& a, Ctrl& c, Group& g, const Ring& ring, int first,
                                    int step, Pos& pos, int& issued) {
-  const Work<X, true> work(a, c.plan.n_act, gridDim.x);
+  const Work<X, true> work(a, c.plan.n_act, step);
   const int row_bytes = a.d * (int)sizeof(X);
   for (int i = first; i < work.total; i += step) {
     const Item w = work.item(i);
@@ -571,7 +574,7 @@ template <typename X>
 __device__ bool produce_up_tokens(const FewArgs& a, Ctrl& c, Group& g, const Ring& ring, int first, int step, Pos& pos,
                                   int& issued) {
   const int lane = threadIdx.x & 31;
-  const Work<X, true> work(a, c.plan.n_act, gridDim.x);
+  const Work<X, true> work(a, c.plan.n_act, step);
   const int row_bytes = a.d * (int)sizeof(X);
   for (int i = first; i < work.total; i += step) {
     const Item w = work.item(i, c.plan);
@@ -595,18 +598,20 @@ __device__ bool produce_up_tokens(const FewArgs& a, Ctrl& c, Group& g, const Rin
   return true;
 }
 
-// few_down's weights and hidden rows: one lane. After its first item a group
-// takes the next that nobody has: SMs reach the memory at rates some 10 %
-// apart. The number is asked for an item ahead.
+// few_down's weights and hidden rows: one lane. The items that fill a group's
+// ring at the start are its own; then it takes the next that nobody has (SMs
+// reach the memory at rates some 10 % apart), asked for an item ahead.
 template <typename X>
 __device__ bool produce_down(const FewMaps& maps, const FewArgs& a, Ctrl& c, Group& g, const Ring& ring, int first,
                              int step, Pos& pos, int& issued) {
-  const Work<X, false> work(a, c.plan.n_act, gridDim.x);
+  const Work<X, false> work(a, c.plan.n_act, step);
   const int row_bytes = a.I * (int)sizeof(X);
+  const int own = 1 + ring.stages * work.split / work.chunks;
   int i = first;
-  while (true) {
+  for (int n = 1;; ++n) {
     const bool more = i < work.total;
-    const int next = more ? step + atomicAdd(a.next, 1) : 0;
+    int next = i + step;
+    if (n >= own && more) next = own * step + atomicAdd(a.next, 1);
     Item w = {};
     if (more) w = work.item(i, c.plan);
     for (int ch = w.c0; ch < (more ? w.c1 : w.c0 + 1); ++ch) {
@@ -764,8 +769,10 @@ __device__ bool multiply(const Item& w, const FewArgs& a, Ctrl& c, Group& g, con
 
 __device__ __forceinline__ float silu_of(float z, const __nv_bfloat16*) { return silu_f32(z); }
 __device__ __forceinline__ float silu_of(float z, const float*) { return z / (1.f + expf(-z)); }
-__device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
-__device__ __forceinline__ void put(float* p, float v) { *p = v; }
+__device__ __forceinline__ void put4(__nv_bfloat16* p, const float4& v) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+}
+__device__ __forceinline__ void put4(float* p, const float4& v) { *reinterpret_cast<float4*>(p) = v; }
 // A hidden value into its row, and what the row leaves of it into the next.
 __device__ __forceinline__ void put_hidden(uint8_t* p, float v, const __nv_bfloat16*) {
   const __nv_bfloat16 hi = __float2bfloat16_rn(v);
@@ -786,7 +793,7 @@ __device__ __forceinline__ float sum_parts(const float* red, int row, int n) {
 template <typename X>
 __device__ void consume_up(const FewArgs& a, Ctrl& c, Group& g, const Ring& ring, float* red2, int group, int first,
                            int step) {
-  const Work<X, true> work(a, c.plan.n_act, gridDim.x);
+  const Work<X, true> work(a, c.plan.n_act, step);
   const int hid_chunks = (a.I * (int)sizeof(X) + kChunk - 1) / kChunk;
   const int tid = threadIdx.x - (group * kGroupWarps + 2) * 32;
   Pos pos;
@@ -808,69 +815,114 @@ __device__ void consume_up(const FewArgs& a, Ctrl& c, Group& g, const Ring& ring
   }
 }
 
-// A group's parts since its last join are counted, and the blocks of columns
+// Waits until `ready` says so, at most limit_ns; false: gave up.
+template <typename F>
+__device__ __forceinline__ bool poll(const FewArgs& a, Ctrl& c, F ready) {
+  const uint64_t t0 = globaltimer_ns();
+  while (!ready()) {
+    __nanosleep(100);
+    if (c.abort) return false;
+    if (globaltimer_ns() - t0 > a.limit_ns) {
+      c.abort = 1;
+      atomicOr(a.status, MOE_DEV_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
+
+// The joins of a group, by a warp of its own: the fence and the atomic's round
+// trip after every item would take as long as its product. Parts that are
+// finished by now are counted, up to 32 at once, and the blocks of columns
 // whose last part that was are added up: part by part of the columns, over a
 // token's experts in slot order.
-// Once for many items: the fence and the atomic's round trip after every item
-// took as long as its product.
 template <typename X>
-__device__ void join(const FewArgs& a, Ctrl& c, Group& g, const Work<X, false>& work, int group, int tid, int n) {
+__device__ void join(const FewArgs& a, Ctrl& c, Group& g, const Work<X, false>& work) {
+  const int lane = threadIdx.x & 31;
   const int R = a.T * a.k, all = c.plan.n_act * work.split;
-  __threadfence();
-  if (tid == 0) g.n_last = 0;
-  math_sync(group);
-  if (tid < n) {
-    const int blk = g.blk[tid];
-    if (atomicAdd(&a.done[blk], 1) == all - 1) g.last[atomicAdd(&g.n_last, 1)] = blk;
-  }
-  math_sync(group);
-  __threadfence();
-  for (int u = tid; u < g.n_last * a.T * kRows; u += kMath) {
-    const int r = u % kRows, q = u / kRows, t = q % a.T, col = g.last[q / a.T] * kRows + r;
-    if (col >= a.d) continue;
-    const float* y = a.y + (size_t)t * a.k * a.d + col;
-    float s = 0.f;
-    for (int p = 0; p < work.split; ++p) {
-#pragma unroll 4
-      for (int j = 0; j < a.k; ++j) s += __ldcg(y + ((size_t)p * R + j) * a.d);
+  int done = 0;
+  while (true) {
+    int f = 0;
+    bool ok = true;
+    if (lane == 0)
+      ok = poll(a, c, [&] {
+        f = g.finished;
+        return f < 0 || f > done;
+      });
+    if (!__all_sync(0xffffffffu, ok)) return;
+    f = __shfl_sync(0xffffffffu, f, 0);
+    __syncwarp();
+    const bool more = f >= 0;
+    const int ready = more ? f : ~f;
+    __threadfence();
+    while (done < ready) {
+      const int n = min(32, ready - done);
+      int blk = -1;
+      if (lane < n) {
+        blk = g.blk[(done + lane) % kJoinQueue];
+        if (atomicAdd(&a.done[blk], 1) != all - 1) blk = -1;
+      }
+      uint32_t last = __ballot_sync(0xffffffffu, blk >= 0);
+      __threadfence();
+      while (last) {
+        const int b = __shfl_sync(0xffffffffu, blk, __ffs(last) - 1);
+        last &= last - 1;
+        for (int u = lane; u < a.T * (kRows / 4); u += 32) {
+          const int t = u / (kRows / 4), col = b * kRows + u % (kRows / 4) * 4;
+          if (col >= a.d) continue;
+          const float* y = a.y + (size_t)t * a.k * a.d + col;
+          float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int p = 0; p < work.split; ++p) {
+#pragma unroll
+            for (int j = 0; j < kMaxTopK; ++j) {
+              if (j < a.k) {
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(y + ((size_t)p * R + j) * a.d));
+                s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+              }
+            }
+          }
+          put4(static_cast<X*>(a.out) + (size_t)t * a.d + col, s);
+        }
+      }
+      done += n;
+      if (lane == 0) g.joined = done;
     }
-    put(static_cast<X*>(a.out) + (size_t)t * a.d + col, s);
+    if (!more) return;
   }
-  math_sync(group);
 }
 
 // few_down's products.
 template <typename X>
-__device__ void consume_down(const FewArgs& a, Ctrl& c, Group& g, const Ring& ring, float* red2, int group) {
-  const Work<X, false> work(a, c.plan.n_act, gridDim.x);
+__device__ void consume_down(const FewArgs& a, Ctrl& c, Group& g, const Ring& ring, float* red2, int group, int step) {
+  const Work<X, false> work(a, c.plan.n_act, step);
   const int tid = threadIdx.x - (group * kGroupWarps + 2) * 32;
   const int R = a.T * a.k;
   Pos pos;
-  int buf = 0, n_blk = 0;
-  while (true) {
+  int buf = 0;
+  for (int n_item = 0;; ++n_item) {
     // the stage says which item begins
     bool ok = __all_sync(0xffffffffu, mbar_wait(&g.full[pos.stage], pos.phase, &c.abort, a.status, a.limit_ns));
     const int i = ok ? g.item[pos.stage] : -1;
-    if (i >= 0) {
-      const Item w = work.item(i, c.plan);
-      float* red = red2 + buf * red_floats<X>();
-      buf ^= 1;
+    const Item w = work.item(max(i, 0), c.plan);
+    float* red = red2 + buf * red_floats<X>();
+    buf ^= 1;
+    if (i >= 0)
       ok = multiply<false>(w, a, c, g, ring, tid >> 5, a.I * (int)sizeof(X), pos, red, static_cast<const X*>(nullptr));
-      if (tid == 0) g.blk[n_blk] = w.blk;
-      if (!math_sync_all(group, ok)) return;
-      const int r = tid & 15, n = tid >> 4, col = w.blk * kRows + r;
-      if (n < w.n && col < a.d)
-        a.y[((size_t)w.part * R + c.plan.tj[w.first + n]) * a.d + col] =
-            c.plan.gate[w.first + n] * sum_parts<X>(red, r, n);
-      if (++n_blk == kMath) {
-        join<X>(a, c, g, work, group, tid, n_blk);
-        n_blk = 0;
+    // behind this barrier the parts of the items before this one are written
+    if (!math_sync_all(group, ok)) return;
+    if (tid < 32) {
+      if (tid == 0) {
+        __threadfence_block();
+        g.finished = i >= 0 ? n_item : ~n_item;
       }
-    } else {
-      if (!math_sync_all(group, ok)) return;
-      if (n_blk) join<X>(a, c, g, work, group, tid, n_blk);
-      return;
+      if (i >= 0 && n_item >= kJoinQueue && !poll(a, c, [&] { return g.joined > n_item - kJoinQueue; })) ok = false;
+      if (tid == 0) g.blk[n_item % kJoinQueue] = w.blk;
     }
+    if (i < 0) return;
+    const int r = tid & 15, n = tid >> 4, col = w.blk * kRows + r;
+    if (n < w.n && col < a.d)
+      a.y[((size_t)w.part * R + c.plan.tj[w.first + n]) * a.d + col] =
+          c.plan.gate[w.first + n] * sum_parts<X>(red, r, n);
   }
 }
 
@@ -893,8 +945,8 @@ __device__ void stream(const FewMaps& maps, const FewArgs& a, Ctrl& c, uint8_t* 
         ok = produce_down<X>(maps, a, c, g, ring, first, step, pos, issued);
       // few_down's first stages, while this kernel ends and that one starts
       if (kUp && ok && group == 0)
-        for (int b = blockIdx.x; b < a.down_blocks; b += gridDim.x)
-          prefetch_weights<X, false>(maps, a, c.plan.expert, c.plan.n_act, b, a.down_blocks);
+        prefetch_weights<X, false>(maps, a, c.plan.expert, c.plan.n_act, blockIdx.x, a.down_blocks,
+                                   a.down_blocks * ring_of<X, false>(smem_ring, c.plan, 0).groups);
       if (!ok || c.abort) drain(a, g, ring, pos, issued);
     }
     __syncwarp();
@@ -903,24 +955,28 @@ __device__ void stream(const FewMaps& maps, const FewArgs& a, Ctrl& c, uint8_t* 
       const bool ok = produce_up_tokens<X>(a, c, g, ring, first, step, pos, issued);
       if (lane == 0 && (!ok || c.abort)) drain(a, g, ring, pos, issued);
       __syncwarp();
+    } else {
+      join<X>(a, c, g, Work<X, false>(a, c.plan.n_act, step));
     }
   } else {
     red += group * 2 * red_floats<X>();
     if constexpr (kUp)
       consume_up<X>(a, c, g, ring, red, group, first, step);
     else
-      consume_down<X>(a, c, g, ring, red, group);
+      consume_down<X>(a, c, g, ring, red, group, step);
   }
 }
 
 template <typename X, bool kUp>
 __device__ __forceinline__ void init_ctrl(Ctrl& c) {
   if (threadIdx.x == 0) {
-    for (int q = 0; q < Traits<X>::kGroups; ++q)
+    for (int q = 0; q < Traits<X>::kGroups; ++q) {
+      c.group[q].finished = c.group[q].joined = 0;
       for (int s = 0; s < kMaxStages; ++s) {
         mbar_init(&c.group[q].full[s], kUp ? 2 : 1);  // few_up has two producers
         mbar_init(&c.group[q].empty[s], kMathWarps);
       }
+    }
     c.abort = 0;
     fence_mbarrier_init();
   }
@@ -941,7 +997,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(threads<X>(),
   uint8_t* ring;
   carve<X>(smem, &c, &red, &ring);
   init_ctrl<X, true>(*c);
-  if (a.likely && threadIdx.x == 32) prefetch_weights<X, true>(maps, a, nullptr, a.E, blockIdx.x, gridDim.x);
+  if (a.likely && threadIdx.x == 32) prefetch_weights<X, true>(maps, a, nullptr, a.E, blockIdx.x, gridDim.x, gridDim.x);
   float* part = reinterpret_cast<float*>(ring);                     // [kCluster][T][E]
   float* scratch = part + (size_t)kCluster * a.T * a.E;             // [kWarps][16][kPassLd]
   const int rank = (int)cluster_ctarank();
@@ -960,7 +1016,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(threads<X>(),
               part, rank);
   cluster_sync();  // all parts are here, and no peer writes here any more
   const bool first = blockIdx.x == 0;
-  choose(a, part, *c, first);
+  choose(a, part, reinterpret_cast<uint32_t*>(scratch), *c, first);
   __syncthreads();
   make_plan(c->plan, c->idx, c->gate, a.T, a.E, a.k);
   if (first && (a.counts || a.aux)) statistics(a, part, *c);

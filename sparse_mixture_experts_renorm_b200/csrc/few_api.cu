@@ -48,8 +48,9 @@ moe_status moe_forward_few(const void* x, const void* w_router, const float* b_r
   if (!x || !w_router || !w_gate || !w_up || !w_down || !out || !topk_idx || !topk_gate || !status_dev)
     return fail(MOE_ERR_INVALID_ARG,
                 "a required pointer (x, weights, out, topk_idx, topk_gate, status_dev) is NULL");
-  if (!aligned16(x) || !aligned16(w_router) || !aligned16(w_gate) || !aligned16(w_up) || !aligned16(w_down))
-    return fail(MOE_ERR_INVALID_ARG, "x and weights must be 16-byte aligned");
+  if (!aligned16(x) || !aligned16(w_router) || !aligned16(w_gate) || !aligned16(w_up) || !aligned16(w_down) ||
+      !aligned16(out))
+    return fail(MOE_ERR_INVALID_ARG, "x, weights and out must be 16-byte aligned");
   const FewWorkspace l = few_layout(T, d, k, I, dtype);
   if (!workspace || workspace_bytes < l.total)
     return fail(MOE_ERR_WORKSPACE, "workspace needs %zu bytes (got %zu%s)", l.total, workspace_bytes,
