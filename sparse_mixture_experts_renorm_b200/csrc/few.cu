@@ -937,7 +937,7 @@ __device__ void stream(const FewMaps& maps, const FewArgs& a, Ctrl& c, uint8_t* 
   Pos pos;
   int issued = 0;
   if (role == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       bool ok;
       if constexpr (kUp)
         ok = produce_up_weights<X>(maps, a, c, g, ring, first, step, pos, issued);

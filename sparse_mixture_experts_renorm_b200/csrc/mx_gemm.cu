@@ -16,11 +16,15 @@
 // columns of K: 128 bytes of codes a row with the 128-byte swizzle, as for 64
 // bf16, and 1024 bytes of scales per 128 rows, which one thread copies to TMEM
 // (tcgen05.cp) in front of the stage's four UMMAs. Both CTAs need the scales
-// of all 256 weight rows. 35 KB a stage, 6 stages.
+// of all 256 weight rows. 35 KB a stage, 6 stages. The issuing thread is the
+// one that elect.sync names: the compiler then keeps the operands in uniform
+// registers. With a test of the lane it moved them there in front of every
+// instruction, 99 cycles for a copy and 135 for a product, and a stage took
+// 1434 cycles of the 512 that its products last; now 553.
 //
 // TMEM: the accumulator takes 256 of 512 columns, the scales 32 columns for
 // each of 4 rotating buffers, so there is no room for a second accumulator of
-// 256 columns. Instead eight epilogue warps first bring their 128 columns into
+// 256 columns. Instead sixteen epilogue warps first bring their 64 columns into
 // registers and release the accumulator, then do the arithmetic and the stores
 // while the next tile's UMMAs run.
 //
@@ -36,7 +40,7 @@ namespace moe {
 namespace {
 
 constexpr int kMxStages = 6;
-constexpr int kMxEpiWarps = 8;
+constexpr int kMxEpiWarps = 16;
 constexpr int kMxThreads = 64 + 32 * kMxEpiWarps;
 constexpr int kHalf = 128 * 128;                // 128 rows x 256 codes
 constexpr int kSfBytes = 3 * kMxStageBytes;     // scales of 128 rows, and of 256 weight rows
@@ -84,6 +88,13 @@ __device__ __forceinline__ uint64_t scales_desc(uint32_t smem_addr) {
   return desc;
 }
 
+// 32 bytes at once, a whole sector.
+__device__ __forceinline__ void store_sector(void* p, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
 struct MxTile {
   int g, m, n, row0, cnt;  // group, 256-row tile, weight block, first row and rows of the group
 };
@@ -128,7 +139,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
   uint64_t* full = bars;               // leader: the stage's bytes of both CTAs
   uint64_t* empty = bars + kMxStages;  // both: stage consumed by the pair's UMMAs
   uint64_t* tfull = bars + 2 * kMxStages;
-  uint64_t* tempty = tfull + 1;        // leader: the epilogue threads of both CTAs
+  uint64_t* tempty = tfull + 1;        // leader: the epilogue warps of both CTAs
   uint64_t* done = tempty + 1;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
@@ -150,7 +161,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
       mbar_init(&empty[s], 1);
     }
     mbar_init(tfull, 1);
-    mbar_init(tempty, 2 * 32 * kMxEpiWarps);
+    mbar_init(tempty, 2 * kMxEpiWarps);
     mbar_init(done, 1);
     *s_abort = 0;
     *s_bad = 0;
@@ -198,7 +209,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------ TMA producer --
-    if (lane == 0) {
+    if (elect_one()) {
       int stage = 0;
       uint32_t phase = 0;
       int issued = 0;
@@ -249,7 +260,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------ MMA issuer (leader only) --
-    if (leader && lane == 0) {
+    if (leader && elect_one()) {
       int stage = 0;
       uint32_t phase = 0;
       uint32_t acc_phase = 0;
@@ -269,17 +280,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
           const int steps = min(4, (K - kb * kMxStageCols + 63) >> 6);  // 64 columns each
           // columns: A's two tiles at 0 and 4, B's two at 8 and 16 (eight
           // columns: the scales of 2 x 128 weight rows)
-          for (int t = 0; t < (steps + 1) >> 1; ++t) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (2 * t >= steps) break;
             tc_cp_scales_pair(sf + 4 * t, scales_desc(ss + 512 * t));
             tc_cp_scales_pair(sf + 8 + 8 * t, scales_desc(ss + kMxStageBytes + 512 * t));
             tc_cp_scales_pair(sf + 12 + 8 * t, scales_desc(ss + 2 * kMxStageBytes + 512 * t));
           }
           const uint64_t adesc = sw128_kmajor_desc(smem_u32(sA + stage * kHalf));
           const uint64_t bdesc = sw128_kmajor_desc(smem_u32(sB + stage * kHalf));
-          for (int s = 0; s < steps; ++s)
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            if (s >= steps) break;
             tc_mma_mxf4_pair(tmem_base, adesc + static_cast<uint64_t>(s * 2), bdesc + static_cast<uint64_t>(s * 2),
                              idesc_mxf4(256, 256, s & 1 ? 2u : 0u), sf + 4 * (s >> 1), sf + 8 + 8 * (s >> 1),
                              (kb | s) != 0 ? 1u : 0u);
+          }
           tc_commit_pair_both(&empty[stage]);
           buf = (buf + 1) & (kSfBufs - 1);
           if (++stage == kMxStages) {
@@ -297,10 +313,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
     __syncwarp();
   } else {
     // --------------------------------------------------------- epilogue --
-    // TMEM lane = a row of this CTA's half of the tile. The two groups of four
-    // warps take columns 0-127 and 128-255, or units 0-63 and 64-127 of the
-    // gate and up halves.
-    const int q = warp & 3, half = (warp - 2) >> 2;
+    // TMEM lane = a row of this CTA's half of the tile. The four groups of
+    // four warps take 64 columns each, or 32 units of the gate and up halves.
+    const int q = warp & 3, part = (warp - 2) >> 2;
+    const bool sectors = !kGateUp && (N & 15) == 0 && (reinterpret_cast<uintptr_t>(out.out) & 31) == 0;
     const uint32_t tempty_leader = map_to_cta(tempty, 0);
     const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
     uint32_t acc_phase = 0;
@@ -310,70 +326,75 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
       if (!__all_sync(0xffffffffu, mbar_wait(tfull, acc_phase, s_abort, status, limit_ns))) break;
       acc_phase ^= 1u;
       tc_fence_after();
-      uint32_t v[4][32];
+      uint32_t v[2][32];
       __syncwarp();
-      if (kGateUp) {
-        tmem_ld_x32(tbase + half * 64, v[0]);
-        tmem_ld_x32(tbase + half * 64 + 32, v[1]);
-        tmem_ld_x32(tbase + 128 + half * 64, v[2]);
-        tmem_ld_x32(tbase + 128 + half * 64 + 32, v[3]);
-      } else {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld_x32(tbase + half * 128 + c * 32, v[c]);
-      }
+      tmem_ld_x32(tbase + (kGateUp ? part * 32 : part * 64), v[0]);
+      tmem_ld_x32(tbase + (kGateUp ? 128 + part * 32 : part * 64 + 32), v[1]);
       tmem_ld_wait();
       tc_fence_before();
-      mbar_arrive_cluster(tempty_leader);
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(tempty_leader);
       const int in_group = t.m * 256 + (int)rank * 128 + rt;
       const bool live = in_group < t.cnt;
       const long long row = t.row0 + in_group;
       if (kGateUp) {
         if (live) {
-          uint32_t sbytes = 0;
+          const int unit0 = t.n * 128 + part * 32;
+          float h[32];
+          uint32_t m = 0;
 #pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            const int unit0 = t.n * 128 + half * 64 + b * 32;
-            float h[32];
-            uint32_t m = 0;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              h[i] = silu_f32(__uint_as_float(v[b][i])) * __uint_as_float(v[2 + b][i]);
-              m = max(m, __float_as_uint(h[i]) & 0x7fffffffu);
-            }
-            if (unit0 < N) {
-              const uint32_t sb = mx_scale_byte(m);
-              const float inv = mx_inv_scale(sb);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) h[i] *= inv;
-              *reinterpret_cast<uint4*>(out.h + (size_t)row * (N / 2) + unit0 / 2) =
-                  make_uint4(mx_pack8(h), mx_pack8(h + 8), mx_pack8(h + 16), mx_pack8(h + 24));
-              sbytes |= sb << (8 * b);
-            }
+          for (int i = 0; i < 32; ++i) {
+            h[i] = silu_f32(__uint_as_float(v[0][i])) * __uint_as_float(v[1][i]);
+            m = max(m, __float_as_uint(h[i]) & 0x7fffffffu);
           }
-          // two of the four bytes of this row in the block's tile of scales
-          *reinterpret_cast<uint16_t*>(
-              out.h_scales + mx_scale_at((size_t)(2 * (s_mt[t.g] + t.m) + (int)rank), mx_stages(N), rt,
-                                         t.n * 4 + half * 2)) = (uint16_t)sbytes;
+          uint32_t sb = 0;
+          if (unit0 < N) {
+            sb = mx_scale_byte(m);
+            const float inv = mx_inv_scale(sb);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) h[i] *= inv;
+            *reinterpret_cast<uint4*>(out.h + (size_t)row * (N / 2) + unit0 / 2) =
+                make_uint4(mx_pack8(h), mx_pack8(h + 8), mx_pack8(h + 16), mx_pack8(h + 24));
+          }
+          // one of the four bytes of this row in the block's tile of scales
+          out.h_scales[mx_scale_at((size_t)(2 * (s_mt[t.g] + t.m) + (int)rank), mx_stages(N), rt, t.n * 4 + part)] =
+              (uint8_t)sb;
         }
       } else if (live) {
         const float gs = out.gate ? out.gate[row] : 1.f;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int n0 = t.n * 256 + half * 128 + c * 32;
+        for (int c = 0; c < 2; ++c) {
+          const int n0 = t.n * 256 + part * 64 + c * 32;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float f[8];
+          for (int i = 0; i < 32; ++i) v[c][i] = __float_as_uint(gs * __uint_as_float(v[c][i]));
+          if (out.f32) {
+            float* dst = static_cast<float*>(out.out) + (size_t)row * N + n0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = gs * __uint_as_float(v[c][8 * j + i]);
-            if (n0 + 8 * j < N) {
-              if (out.f32) {
-                float4* dst = reinterpret_cast<float4*>(static_cast<float*>(out.out) + (size_t)row * N + n0 + 8 * j);
-                dst[0] = make_float4(f[0], f[1], f[2], f[3]);
-                dst[1] = make_float4(f[4], f[5], f[6], f[7]);
+            for (int j = 0; j < 4; ++j) {
+              if (n0 + 8 * j < N) {
+                const uint32_t w[8] = {v[c][8 * j],     v[c][8 * j + 1], v[c][8 * j + 2], v[c][8 * j + 3],
+                                       v[c][8 * j + 4], v[c][8 * j + 5], v[c][8 * j + 6], v[c][8 * j + 7]};
+                if (sectors) {
+                  store_sector(dst + 8 * j, w);
+                } else {
+                  reinterpret_cast<uint4*>(dst + 8 * j)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                  reinterpret_cast<uint4*>(dst + 8 * j)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                }
+              }
+            }
+          } else {
+            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(out.out) + (size_t)row * N + n0;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              uint32_t w[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                w[i] = pack_bf16x2(__uint_as_float(v[c][16 * j + 2 * i]), __uint_as_float(v[c][16 * j + 2 * i + 1]));
+              if (sectors && n0 + 16 * j < N) {
+                store_sector(dst + 16 * j, w);
               } else {
-                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out.out) + (size_t)row * N + n0 + 8 * j) =
-                    make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                               pack_bf16x2(f[6], f[7]));
+                if (n0 + 16 * j < N) reinterpret_cast<uint4*>(dst + 16 * j)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                if (n0 + 16 * j + 8 < N) reinterpret_cast<uint4*>(dst + 16 * j)[1] = make_uint4(w[4], w[5], w[6], w[7]);
               }
             }
           }
