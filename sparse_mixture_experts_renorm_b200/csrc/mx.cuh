@@ -63,13 +63,19 @@ __device__ __forceinline__ uint32_t mx_pack8(const float* v) {
   return r;
 }
 
-// The value of one E2M1 code: magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6.
-__device__ __forceinline__ float mx_value(uint32_t code) {
-  const uint32_t m = code & 7u;
-  // 1, 1.5, 2, 3, 4, 6 are (exponent, mantissa bit) of a float; 0 and 0.5 are
-  // the subnormal pair
-  const float a = m < 2u ? 0.5f * (float)m : __uint_as_float((126u << 23) + (m << 22));
-  return code & 8u ? -a : a;
+// The values of eight E2M1 codes as bf16, element i in half i % 2 of w[i / 2].
+// Byte permutes look the two bytes of 0, 0.5, 1, 1.5, 2, 3, 4, 6 up, four
+// codes at once.
+__device__ __forceinline__ void mx_values8(uint32_t code, uint32_t (&w)[4]) {
+  const uint32_t even = (code << 4) & 0x80808080u, odd = code & 0x80808080u;  // signs
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t sel = (code >> (16 * i)) & 0x7777u;
+    const uint32_t lo = __byte_perm(0xC0800000u, 0xC0804000u, sel);
+    const uint32_t hi = __byte_perm(0x3F3F3F00u, 0x40404040u, sel) | __byte_perm(even, odd, i ? 0x7362 : 0x5140);
+    w[2 * i] = __byte_perm(lo, hi, 0x5140);
+    w[2 * i + 1] = __byte_perm(lo, hi, 0x7362);
+  }
 }
 
 }  // namespace moe

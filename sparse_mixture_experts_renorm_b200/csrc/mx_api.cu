@@ -199,7 +199,7 @@ static moe_status convert_args(const void* a, const void* data, const void* scal
     if (!a || !data || !scales) return fail(MOE_ERR_INVALID_ARG, "%s: a required pointer is NULL", what);
     if (!aligned16(a) || !aligned16(data) || !aligned16(scales))
       return fail(MOE_ERR_INVALID_ARG, "%s: values, codes and scales must be 16-byte aligned", what);
-    if ((offsets ? 1ll : (long long)groups) * rows * mx_stage_count(cols) / 32 >= kIntMax)
+    if ((offsets ? 1ll : (long long)groups) * rows * (cols / 8) / 1024 >= kIntMax)
       return fail(MOE_ERR_UNSUPPORTED, "%s: the matrix is too large for one call", what);
   }
   *tile_rows = scale_bytes / ((size_t)mx_stage_count(cols) * 1024);

@@ -4,18 +4,20 @@
 //   code_i = E2M1(x_i / 2^s), round to nearest even, at most 6;   x~_i = code_i 2^s
 //
 // Both directions only move memory: a row of C columns is C * (2 or 4) bytes
-// on one side and C / 2 + C / 32 on the other. A warp takes 256 columns of a
-// row at a time, eight consecutive columns a lane (16 or 32 bytes of x, 4 of
-// codes), so every access of a warp is one contiguous run; four lanes share a
-// block and agree on its scale with two shuffles. Four such pieces are in
-// flight per warp.
+// on one side and C / 2 + C / 32 on the other. A lane takes 32 bytes of x at
+// a time and the lanes of a warp follow one another through the
+// matrix, across the ends of rows, so that narrow rows are read as evenly as
+// wide ones; the lanes of a block agree on its scale by shuffles.
+// Four such pieces are in flight per lane. With 8 columns a lane and a warp
+// per 256 columns of one row the instructions (divisions, shuffles) bound it:
+// 8 x 14336 x 4096 bf16 took 266 us to quantise and 254 back.
 #include "mx.cuh"
 
 namespace moe {
 namespace {
 
 constexpr int kQThreads = 256;
-constexpr int kQUnits = 4;  // 256-column pieces per warp in flight
+constexpr int kQUnits = 4;  // pieces per lane in flight
 
 // Where the groups of rows lie: group g's rows are [off[g], off[g+1]) and its
 // scales start at tile row tile[g].
@@ -68,38 +70,148 @@ __device__ __forceinline__ bool place_row(const Groups& s, int G, int row, size_
   return true;
 }
 
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* v) {
-  const uint4 u = __ldcs(reinterpret_cast<const uint4*>(p));
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+// A lane's pieces, 32 apart, with their place among the scales.
+// Only the first one takes divisions, unless rows are shorter than a warp's
+// step.
+struct Pieces {
+  uint32_t row, k;          // row, and piece of it
+  uint32_t in;              // row in its group (dense)
+  size_t group_row;         // first tile row of its group (dense)
+  uint32_t per, rows, group_tiles;
+  __device__ __forceinline__ Pieces(unsigned long long u, uint32_t per_, uint32_t rows_, uint32_t group_tiles_)
+      : per(per_), rows(rows_), group_tiles(group_tiles_) {
+    row = u >> 32 ? (uint32_t)(u / per) : (uint32_t)u / per;
+    k = (uint32_t)(u - (unsigned long long)row * per);
+    const uint32_t g = row / rows;
+    in = row - g * rows;
+    group_row = (size_t)g * group_tiles;
+  }
+  __device__ __forceinline__ void next() {
+    k += 32;
+    if (k < per) return;
+    uint32_t n = 1;
+    if (per < 32) n = k / per;
+    k -= n * per;
+    row += n;
+    in += n;
+    if (in < rows) return;
+    const uint32_t g = per < 32 ? in / rows : 1u;
+    in -= g * rows;
+    group_row += (size_t)g * group_tiles;
+  }
+  // False for a row of no group, or one whose scales there is no room for.
+  __device__ __forceinline__ bool place(const Groups& s, bool ragged, int G, size_t tile_rows, size_t* tile_row,
+                                        int* r) const {
+    bool live = true;
+    if (ragged) {
+      live = place_row(s, G, (int)row, tile_row, r);
+    } else {
+      *tile_row = group_row + (in >> 7);
+      *r = (int)(in & 127);
+    }
+    return live && *tile_row < tile_rows;
+  }
+};
+
+// 32 bytes to or from memory that is used once, a whole sector at once where
+// the address allows (rows are multiples of 32 bytes, so `wide` is a question
+// of the first one's).
+__device__ __forceinline__ void load_sector(uint32_t (&w)[8], const void* p, bool wide) {
+  if (wide) {
+    asm volatile("ld.global.cs.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                 : "l"(p));
+  } else {
+    const uint4 a = __ldcs(static_cast<const uint4*>(p)), b = __ldcs(static_cast<const uint4*>(p) + 1);
+    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
   }
 }
-__device__ __forceinline__ void load8(const float* p, float* v) {
-  const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-}
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* v) {
-  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                                            pack_bf16x2(v[6], v[7]));
-}
-__device__ __forceinline__ void store8(float* p, const float* v) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+__device__ __forceinline__ void store_sector(void* p, const uint32_t (&w)[8], bool wide) {
+  if (wide) {
+    asm volatile("st.global.cs.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]),
+                 "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    __stcs(static_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
+    __stcs(static_cast<uint4*>(p) + 1, make_uint4(w[4], w[5], w[6], w[7]));
+  }
 }
 
-// The tile row and row in it of a row of [G, rows] with every group padded.
-__device__ __forceinline__ void place_dense(long long row, int rows, int group_tiles, size_t* tile_row, int* r) {
-  const long long g = row / rows;
-  const int in = (int)(row - g * rows);
-  *tile_row = (size_t)g * group_tiles + (size_t)(in >> 7);
-  *r = in & 127;
+// A piece in registers: 16 bf16 or 8 fp32, and its codes.
+template <typename T>
+struct Piece;
+template <>
+struct Piece<__nv_bfloat16> {
+  static constexpr int kCols = 16;
+  using Codes = uint2;
+  uint32_t w[8];
+  // The largest magnitude's bits as those of a float.
+  __device__ __forceinline__ uint32_t amax() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+    return max(m << 16, m & 0xffff0000u);
+  }
+  // Times a power of two: exact where it is not so small that its code is 0.
+  __device__ __forceinline__ Codes codes(float inv) const {
+    const __nv_bfloat162 s = __float2bfloat162_rn(inv);
+    float q[16];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const __nv_bfloat162 t = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]), s);
+      const uint32_t b = *reinterpret_cast<const uint32_t*>(&t);
+      q[2 * i] = __uint_as_float(b << 16);
+      q[2 * i + 1] = __uint_as_float(b & 0xffff0000u);
+    }
+    return make_uint2(mx_pack8(q), mx_pack8(q + 8));
+  }
+  __device__ __forceinline__ void values(const Codes& c, float scale) {
+    const __nv_bfloat162 s = __float2bfloat162_rn(scale);
+    uint32_t a[4], b[4];
+    mx_values8(c.x, a);
+    mx_values8(c.y, b);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const __nv_bfloat162 t = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(i < 4 ? &a[i] : &b[i - 4]), s);
+      w[i] = *reinterpret_cast<const uint32_t*>(&t);
+    }
+  }
+};
+template <>
+struct Piece<float> {
+  static constexpr int kCols = 8;
+  using Codes = uint32_t;
+  uint32_t w[8];
+  __device__ __forceinline__ uint32_t amax() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, w[i] & 0x7fffffffu);
+    return m;
+  }
+  __device__ __forceinline__ Codes codes(float inv) const {
+    float q[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = __uint_as_float(w[i]) * inv;
+    return mx_pack8(q);
+  }
+  __device__ __forceinline__ void values(const Codes& c, float s) {
+    uint32_t a[4];
+    mx_values8(c, a);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      w[2 * i] = __float_as_uint(__uint_as_float(a[i] << 16) * s);
+      w[2 * i + 1] = __float_as_uint(__uint_as_float(a[i] & 0xffff0000u) * s);
+    }
+  }
+};
+
+// The first piece of this lane.
+__device__ __forceinline__ unsigned long long first_piece() {
+  return ((unsigned long long)blockIdx.x * (kQThreads / 32) + (threadIdx.x >> 5)) * (kQUnits * 32) + (threadIdx.x & 31);
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kQThreads) mx_quantize_kernel(const T* __restrict__ x, long long n_rows, int rows,
+__global__ void __launch_bounds__(kQThreads) mx_quantize_kernel(const T* __restrict__ x, uint32_t n_rows, int rows,
                                                                 int cols, const int32_t* __restrict__ offsets, int G,
                                                                 int group_tiles, size_t tile_rows,
                                                                 uint8_t* __restrict__ data,
@@ -107,57 +219,43 @@ __global__ void __launch_bounds__(kQThreads) mx_quantize_kernel(const T* __restr
   __shared__ Groups s_g;
   pdl_wait();
   if (offsets) load_groups(s_g, offsets, G);
-  const int lane = threadIdx.x & 31;
   const int st = mx_stages(cols);
-  const long long units = n_rows * st;
-  const long long u0 = ((long long)blockIdx.x * (kQThreads / 32) + (threadIdx.x >> 5)) * kQUnits;
-  float v[kQUnits][8];
+  const unsigned long long u = first_piece();
+  constexpr int kCols = Piece<T>::kCols, kLanes = 32 / kCols;  // lanes of a block
+  Pieces p(u, cols / kCols, rows, group_tiles);
+  Pieces q = p;
+  const bool wide = (reinterpret_cast<uintptr_t>(x) & 31) == 0;
+  Piece<T> v[kQUnits];
 #pragma unroll
   for (int i = 0; i < kQUnits; ++i) {
-    const long long u = u0 + i, row = u / st;
-    const int c = (int)(u - row * st) * kMxStageCols + lane * 8;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
-    if (u < units && c < cols) load8(x + row * cols + c, v[i]);
+    if (q.row < n_rows) load_sector(v[i].w, x + (u + 32 * i) * kCols, wide);
+    q.next();
   }
 #pragma unroll
   for (int i = 0; i < kQUnits; ++i) {
-    const long long u = u0 + i;
-    if (u >= units) break;
-    const long long row = u / st;
-    const int kb = (int)(u - row * st);
-    const int c = kb * kMxStageCols + lane * 8;
-    uint32_t m = 0;
+    const bool have = p.row < n_rows;
+    uint32_t m = have ? v[i].amax() : 0u;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[i][j]) & 0x7fffffffu);
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    const uint32_t sb = mx_scale_byte(m);
-    const float inv = mx_inv_scale(sb);
-    float q[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) q[j] = v[i][j] * inv;
-    // four blocks' bytes in one word, gathered over 16 lanes
-    uint32_t word = sb << (8 * ((lane >> 2) & 3));
-    word |= __shfl_xor_sync(0xffffffffu, word, 4);
-    word |= __shfl_xor_sync(0xffffffffu, word, 8);
+    for (int o = 1; o < kLanes; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
     size_t tile_row = 0;
     int r = 0;
-    bool live = true;
-    if (offsets)
-      live = place_row(s_g, G, (int)row, &tile_row, &r);
-    else
-      place_dense(row, rows, group_tiles, &tile_row, &r);
-    if (!live || tile_row >= tile_rows) continue;
-    if (c < cols) *reinterpret_cast<uint32_t*>(data + row * (cols / 2) + c / 2) = mx_pack8(q);
-    if ((lane & 15) == 0)
-      *reinterpret_cast<uint32_t*>(scales + mx_scale_at(tile_row, st, r, kb * 8 + (lane >> 2))) = word;
+    if (have && p.place(s_g, offsets != nullptr, G, tile_rows, &tile_row, &r)) {
+      const uint32_t sb = mx_scale_byte(m);
+      *reinterpret_cast<typename Piece<T>::Codes*>(data + (u + 32 * i) * (kCols / 2)) = v[i].codes(mx_inv_scale(sb));
+      if (p.k % kLanes == 0) {
+        const int b = (int)p.k / kLanes;
+        scales[mx_scale_at(tile_row, st, r, b)] = (uint8_t)sb;
+        if (b == cols / 32 - 1)  // zeros behind the row's last
+          for (int z = b + 1; z < 8 * st; ++z) scales[mx_scale_at(tile_row, st, r, z)] = 0;
+      }
+    }
+    p.next();
   }
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kQThreads) mx_dequantize_kernel(const uint8_t* __restrict__ data,
-                                                                  const uint8_t* __restrict__ scales, long long n_rows,
+                                                                  const uint8_t* __restrict__ scales, uint32_t n_rows,
                                                                   int rows, int cols,
                                                                   const int32_t* __restrict__ offsets, int G,
                                                                   int group_tiles, size_t tile_rows,
@@ -165,51 +263,41 @@ __global__ void __launch_bounds__(kQThreads) mx_dequantize_kernel(const uint8_t*
   __shared__ Groups s_g;
   pdl_wait();
   if (offsets) load_groups(s_g, offsets, G);
-  const int lane = threadIdx.x & 31;
   const int st = mx_stages(cols);
-  const long long units = n_rows * st;
-  const long long u0 = ((long long)blockIdx.x * (kQThreads / 32) + (threadIdx.x >> 5)) * kQUnits;
-  uint32_t code[kQUnits], sb[kQUnits];
+  const unsigned long long u = first_piece();
+  constexpr int kCols = Piece<T>::kCols, kLanes = 32 / kCols;  // lanes of a block
+  Pieces p(u, cols / kCols, rows, group_tiles);
+  const bool wide = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
+  typename Piece<T>::Codes code[kQUnits];
+  uint32_t sb[kQUnits];
 #pragma unroll
   for (int i = 0; i < kQUnits; ++i) {
-    const long long u = u0 + i, row = u / st;
-    const int kb = (int)(u - row * st);
-    const int c = kb * kMxStageCols + lane * 8;
-    code[i] = sb[i] = 0;
-    if (u < units && c < cols) {
-      size_t tile_row = 0;
-      int r = 0;
-      bool live = true;
-      if (offsets)
-        live = place_row(s_g, G, (int)row, &tile_row, &r);
-      else
-        place_dense(row, rows, group_tiles, &tile_row, &r);
-      if (live && tile_row < tile_rows) {
-        code[i] = __ldcs(reinterpret_cast<const uint32_t*>(data + row * (cols / 2) + c / 2));
-        sb[i] = 0x100u | __ldg(scales + mx_scale_at(tile_row, st, r, kb * 8 + (lane >> 2)));
-      }
+    sb[i] = 0;
+    size_t tile_row = 0;
+    int r = 0;
+    if (p.row < n_rows && p.place(s_g, offsets != nullptr, G, tile_rows, &tile_row, &r)) {
+      code[i] = __ldcs(reinterpret_cast<const typename Piece<T>::Codes*>(data + (u + 32 * i) * (kCols / 2)));
+      sb[i] = 0x100u | __ldg(scales + mx_scale_at(tile_row, st, r, (int)p.k / kLanes));
     }
+    p.next();
   }
 #pragma unroll
-  for (int i = 0; i < kQUnits; ++i) {
-    const long long u = u0 + i, row = u / st;
-    const int c = (int)(u - row * st) * kMxStageCols + lane * 8;
-    if (!(sb[i] & 0x100u)) continue;
-    const float s = mx_scale_value(sb[i] & 0xffu);
-    float v[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = mx_value(code[i] >> (4 * j)) * s;
-    store8(out + row * cols + c, v);
-  }
+  for (int i = 0; i < kQUnits; ++i)
+    if (sb[i] & 0x100u) {
+      Piece<T> v;
+      v.values(code[i], mx_scale_value(sb[i] & 0xffu));
+      store_sector(out + (u + 32 * i) * kCols, v.w, wide);
+    }
 }
 
 }  // namespace
 
-cudaError_t launch_mx_quantize(moe_dtype dtype, const void* x, long long n_rows, int rows, int cols,
+cudaError_t launch_mx_quantize(moe_dtype dtype, const void* x, long long total_rows, int rows, int cols,
                                const int32_t* offsets, int G, int group_tiles, size_t tile_rows, void* data,
                                void* scales, cudaStream_t stream) {
-  const long long units = n_rows * mx_stages(cols);
-  const int per = (kQThreads / 32) * kQUnits;
+  const long long units = total_rows * (cols / (dtype == MOE_BF16 ? Piece<__nv_bfloat16>::kCols : Piece<float>::kCols));
+  const uint32_t n_rows = (uint32_t)total_rows;  // below 2^31
+  const int per = kQThreads * kQUnits;
   const dim3 grid((unsigned)((units + per - 1) / per));
   uint8_t* d = static_cast<uint8_t*>(data);
   uint8_t* s = static_cast<uint8_t*>(scales);
@@ -221,11 +309,12 @@ cudaError_t launch_mx_quantize(moe_dtype dtype, const void* x, long long n_rows,
                     rows, cols, offsets, G, group_tiles, tile_rows, d, s);
 }
 
-cudaError_t launch_mx_dequantize(moe_dtype dtype, const void* data, const void* scales, long long n_rows, int rows,
+cudaError_t launch_mx_dequantize(moe_dtype dtype, const void* data, const void* scales, long long total_rows, int rows,
                                  int cols, const int32_t* offsets, int G, int group_tiles, size_t tile_rows, void* out,
                                  cudaStream_t stream) {
-  const long long units = n_rows * mx_stages(cols);
-  const int per = (kQThreads / 32) * kQUnits;
+  const long long units = total_rows * (cols / (dtype == MOE_BF16 ? Piece<__nv_bfloat16>::kCols : Piece<float>::kCols));
+  const uint32_t n_rows = (uint32_t)total_rows;  // below 2^31
+  const int per = kQThreads * kQUnits;
   const dim3 grid((unsigned)((units + per - 1) / per));
   const uint8_t* d = static_cast<const uint8_t*>(data);
   const uint8_t* s = static_cast<const uint8_t*>(scales);
