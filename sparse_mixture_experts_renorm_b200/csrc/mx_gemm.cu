@@ -16,7 +16,7 @@
 // columns of K: 128 bytes of codes a row with the 128-byte swizzle, as for 64
 // bf16, and 1024 bytes of scales per 128 rows, which one thread copies to TMEM
 // (tcgen05.cp) in front of the stage's four UMMAs. Both CTAs need the scales
-// of all 256 weight rows. 35 KB a stage, 6 stages. The issuing thread is the
+// of all 256 weight rows. 35 KB a stage, 5 stages. The issuing thread is the
 // one that elect.sync names: the compiler then keeps the operands in uniform
 // registers. With a test of the lane it moved them there in front of every
 // instruction, 99 cycles for a copy and 135 for a product, and a stage took
@@ -39,12 +39,16 @@
 namespace moe {
 namespace {
 
-constexpr int kMxStages = 6;
+constexpr int kMxStages = 5;
 constexpr int kMxEpiWarps = 16;
 constexpr int kMxThreads = 64 + 32 * kMxEpiWarps;
 constexpr int kHalf = 128 * 128;                // 128 rows x 256 codes
 constexpr int kSfBytes = 3 * kMxStageBytes;     // scales of 128 rows, and of 256 weight rows
-constexpr int kMxSmem = kMxStages * (2 * kHalf + kSfBytes) + 1024 + 4096;
+// Results pass through shared memory on their way out: 64 bytes of each of a
+// warp's 32 rows, 80 apart so that eight rows' 16 bytes fall on all banks.
+constexpr int kOutPitch = 80;
+constexpr int kOutWarp = 32 * kOutPitch;
+constexpr int kMxSmem = kMxStages * (2 * kHalf + kSfBytes) + kMxEpiWarps * kOutWarp + 1024 + 4096;
 constexpr uint32_t kStageTx = 2u * (2 * kHalf + kSfBytes);  // both CTAs
 constexpr uint32_t kSfCol = 256;                // first TMEM column of the scales
 constexpr int kSfBufs = 4, kSfCols = 32;
@@ -88,12 +92,8 @@ __device__ __forceinline__ uint64_t scales_desc(uint32_t smem_addr) {
   return desc;
 }
 
-// 32 bytes at once, a whole sector.
-__device__ __forceinline__ void store_sector(void* p, const uint32_t (&v)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
-}
+// A barrier of the four epilogue warps of one lane quarter.
+__device__ __forceinline__ void quarter_sync(int q) { asm volatile("bar.sync %0, 128;" ::"r"(1 + q) : "memory"); }
 
 struct MxTile {
   int g, m, n, row0, cnt;  // group, 256-row tile, weight block, first row and rows of the group
@@ -135,7 +135,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
   uint8_t* sA = smem;
   uint8_t* sB = smem + kMxStages * kHalf;
   uint8_t* sS = smem + 2 * kMxStages * kHalf;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kMxStages * (2 * kHalf + kSfBytes));
+  uint8_t* sOut = smem + kMxStages * (2 * kHalf + kSfBytes);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sOut + kMxEpiWarps * kOutWarp);
   uint64_t* full = bars;               // leader: the stage's bytes of both CTAs
   uint64_t* empty = bars + kMxStages;  // both: stage consumed by the pair's UMMAs
   uint64_t* tfull = bars + 2 * kMxStages;
@@ -316,7 +317,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
     // TMEM lane = a row of this CTA's half of the tile. The four groups of
     // four warps take 64 columns each, or 32 units of the gate and up halves.
     const int q = warp & 3, part = (warp - 2) >> 2;
-    const bool sectors = !kGateUp && (N & 15) == 0 && (reinterpret_cast<uintptr_t>(out.out) & 31) == 0;
+    uint8_t* mine = sOut + (warp - 2) * kOutWarp;
     const uint32_t tempty_leader = map_to_cta(tempty, 0);
     const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
     uint32_t acc_phase = 0;
@@ -333,70 +334,81 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
       tmem_ld_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(tempty_leader);
-      const int in_group = t.m * 256 + (int)rank * 128 + rt;
-      const bool live = in_group < t.cnt;
-      const long long row = t.row0 + in_group;
+      if (lane == 0) mbar_arrive_cluster_cta(tempty_leader);
+      const int first = t.m * 256 + (int)rank * 128 + q * 32;  // this warp's first row in its group
+      if (first >= t.cnt) continue;  // none of them exists (the other parts of the quarter leave as well)
       if (kGateUp) {
-        if (live) {
-          const int unit0 = t.n * 128 + part * 32;
-          float h[32];
-          uint32_t m = 0;
+        const int unit0 = t.n * 128 + part * 32;
+        float h[32];
+        uint32_t m = 0;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            h[i] = silu_f32(__uint_as_float(v[0][i])) * __uint_as_float(v[1][i]);
-            m = max(m, __float_as_uint(h[i]) & 0x7fffffffu);
-          }
-          uint32_t sb = 0;
-          if (unit0 < N) {
-            sb = mx_scale_byte(m);
-            const float inv = mx_inv_scale(sb);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) h[i] *= inv;
-            *reinterpret_cast<uint4*>(out.h + (size_t)row * (N / 2) + unit0 / 2) =
-                make_uint4(mx_pack8(h), mx_pack8(h + 8), mx_pack8(h + 16), mx_pack8(h + 24));
-          }
-          // one of the four bytes of this row in the block's tile of scales
-          out.h_scales[mx_scale_at((size_t)(2 * (s_mt[t.g] + t.m) + (int)rank), mx_stages(N), rt, t.n * 4 + part)] =
-              (uint8_t)sb;
+        for (int i = 0; i < 32; ++i) {
+          h[i] = silu_f32(__uint_as_float(v[0][i])) * __uint_as_float(v[1][i]);
+          m = max(m, __float_as_uint(h[i]) & 0x7fffffffu);
         }
-      } else if (live) {
-        const float gs = out.gate ? out.gate[row] : 1.f;
+        const uint32_t sb = unit0 < N ? mx_scale_byte(m) : 0u;
+        const float inv = mx_inv_scale(sb);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) h[i] *= inv;
+        // the quarter's four parts side by side: 64 bytes of codes and four of
+        // scales a row
+        uint8_t* rows = sOut + q * (32 * kOutPitch);
+        uint8_t* sc = sOut + 4 * (32 * kOutPitch) + q * 4;
+        quarter_sync(q);
+        *reinterpret_cast<uint4*>(rows + lane * kOutPitch + part * 16) =
+            make_uint4(mx_pack8(h), mx_pack8(h + 8), mx_pack8(h + 16), mx_pack8(h + 24));
+        sc[lane * 16 + part] = (uint8_t)sb;
+        quarter_sync(q);
+        const int r = part * 8 + (lane >> 2), at = t.n * 64 + (lane & 3) * 16;
+        if (first + r < t.cnt && at < N / 2)
+          *reinterpret_cast<uint4*>(out.h + (size_t)(t.row0 + first + r) * (N / 2) + at) =
+              *reinterpret_cast<const uint4*>(rows + r * kOutPitch + (lane & 3) * 16);
+        if (part == 0)
+          *reinterpret_cast<uint32_t*>(out.h_scales + mx_scale_at((size_t)(2 * (s_mt[t.g] + t.m) + (int)rank), mx_stages(N),
+                                                                 rt, t.n * 4)) =
+              *reinterpret_cast<const uint32_t*>(sc + lane * 16);
+      } else {
+        const float gs = out.gate && first + lane < t.cnt ? out.gate[t.row0 + first + lane] : 1.f;
+        const int el = out.f32 ? 4 : 2;
+        const int cols = 64 / el;  // of a pass
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const int n0 = t.n * 256 + part * 64 + c * 32;
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[c][i] = __float_as_uint(gs * __uint_as_float(v[c][i]));
-          if (out.f32) {
-            float* dst = static_cast<float*>(out.out) + (size_t)row * N + n0;
+        }
+        auto pass = [&](int c0, const uint4& a, const uint4& b, const uint4& d, const uint4& e) {
+          __syncwarp();
+          uint4* w = reinterpret_cast<uint4*>(mine + lane * kOutPitch);
+          w[0] = a, w[1] = b, w[2] = d, w[3] = e;
+          __syncwarp();
+          const int col = t.n * 256 + part * 64 + c0 + (lane & 3) * (cols / 4);
+          uint8_t* dst = static_cast<uint8_t*>(out.out) + ((size_t)(t.row0 + first) * N + col) * el;
+          if (col < N) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              if (n0 + 8 * j < N) {
-                const uint32_t w[8] = {v[c][8 * j],     v[c][8 * j + 1], v[c][8 * j + 2], v[c][8 * j + 3],
-                                       v[c][8 * j + 4], v[c][8 * j + 5], v[c][8 * j + 6], v[c][8 * j + 7]};
-                if (sectors) {
-                  store_sector(dst + 8 * j, w);
-                } else {
-                  reinterpret_cast<uint4*>(dst + 8 * j)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                  reinterpret_cast<uint4*>(dst + 8 * j)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-                }
-              }
+            for (int i = 0; i < 4; ++i) {
+              const int r = i * 8 + (lane >> 2);
+              if (first + r < t.cnt)
+                *reinterpret_cast<uint4*>(dst + (size_t)r * N * el) =
+                    *reinterpret_cast<const uint4*>(mine + r * kOutPitch + (lane & 3) * 16);
             }
-          } else {
-            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(out.out) + (size_t)row * N + n0;
+          }
+        };
+        if (out.f32) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              uint32_t w[8];
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t* w = &v[c >> 1][(c & 1) * 16];
+            pass(c * 16, make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7]),
+                 make_uint4(w[8], w[9], w[10], w[11]), make_uint4(w[12], w[13], w[14], w[15]));
+          }
+        } else {
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                w[i] = pack_bf16x2(__uint_as_float(v[c][16 * j + 2 * i]), __uint_as_float(v[c][16 * j + 2 * i + 1]));
-              if (sectors && n0 + 16 * j < N) {
-                store_sector(dst + 16 * j, w);
-              } else {
-                if (n0 + 16 * j < N) reinterpret_cast<uint4*>(dst + 16 * j)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                if (n0 + 16 * j + 8 < N) reinterpret_cast<uint4*>(dst + 16 * j)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-              }
-            }
+          for (int c = 0; c < 2; ++c) {
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              w[i] = pack_bf16x2(__uint_as_float(v[c][2 * i]), __uint_as_float(v[c][2 * i + 1]));
+            pass(c * 32, make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7]),
+                 make_uint4(w[8], w[9], w[10], w[11]), make_uint4(w[12], w[13], w[14], w[15]));
           }
         }
       }
