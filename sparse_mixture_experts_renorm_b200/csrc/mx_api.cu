@@ -2,6 +2,7 @@
 // checks, the workspace of the experts and the launch sequence
 //   (router or count) -> scan -> dispatch + quantise -> gate/up + SwiGLU +
 //   quantise -> down -> combine
+// (without a router the dispatch does the scan, and for few choices the count)
 // on the caller's stream. Nothing here synchronises the host or allocates.
 #include "mx_internal.h"
 
@@ -13,7 +14,7 @@ constexpr long long kIntMax = (1ll << 31) - 1;
 
 // Byte offsets inside the workspace of the experts.
 struct MxWorkspace {
-  size_t status, offsets, counts, mtile, aux, blk_cnt, blk_psum, lrank, inv, rgate, xq, xq_sc, h, h_sc, y, total;
+  size_t status, offsets, counts, mtile, aux, blk_cnt, blk_psum, lrank, inv, rgate, xq, xq_sc, h, h_sc, y, y_exp, total;
   long long tiles;  // tile rows of the scales of the dispatched rows
 };
 
@@ -39,6 +40,7 @@ MxWorkspace mx_layout(int T, int d, int E, int k, int I) {
   w.h = o;        o = align256(o + R * (size_t)(I / 2));
   w.h_sc = o;     o = align256(o + (size_t)w.tiles * mx_stage_count(I) * 1024);
   w.y = o;        o = align256(o + 2 * R * (size_t)d);
+  w.y_exp = o;    o = align256(o + 8 * R * (size_t)mx_stage_count(d));
   w.total = o;
   return w;
 }
@@ -131,31 +133,46 @@ moe_status mx_layer(const void* x, const void* w_router, const float* b_router, 
       !weight_maps(&down, w->down, w->down_scales, w->down, w->down_scales, E, d, I))
     return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed (driver entry point unavailable or bad pointer)");
 
-  bool scanned = false;
-  int rb = kRouterTokensTc;
+  MxDispatch md = {};
+  md.scan = kScanDone;
+  md.rb = kRouterTokensTc;
+  const int nb = (T + kRouterTokensTc - 1) / kRouterTokensTc;
+  bool scan = false;  // by its kernel
   if (route) {
-    rb = router_block_tokens(dtype);
+    md.rb = router_block_tokens(dtype);
     RouterNorm rn = {};
     RouterScan rs;
     rs.counts = cnt;
     rs.offsets = offsets;
     rs.mtile = mtile;
     rs.aux = aux_p;
-    scanned = router_does_scan(T, E, dtype);
+    scan = !router_does_scan(T, E, dtype);
     err = launch_router(dtype, x, w_router, b_router, T, d, E, k, renorm, rn, topk_idx, topk_gate, lrank, blk_cnt,
                         blk_psum, nullptr, rs, status, stream);
     if (err != cudaSuccess) return fail_cuda(err, "router kernel");
+  } else if (R <= kScanAllMost) {
+    md.scan = kScanAll;
   } else {
+    if ((long long)nb * E <= kScanBlocksMost)
+      md.scan = kScanBlocks;
+    else
+      scan = true;
     err = launch_mx_count(topk_idx, T, E, k, lrank, blk_cnt, blk_psum, status, stream);
     if (err != cudaSuccess) return fail_cuda(err, "count kernel");
   }
-  if (!scanned) {
-    err = launch_route_scan((T + rb - 1) / rb, T, E, k, -1, 0, blk_cnt, blk_psum, nullptr, cnt, offsets, mtile, aux_p,
+  if (scan) {
+    err = launch_route_scan((T + md.rb - 1) / md.rb, T, E, k, -1, 0, blk_cnt, blk_psum, nullptr, cnt, offsets, mtile, aux_p,
                             nullptr, nullptr, nullptr, 0, stream);
     if (err != cudaSuccess) return fail_cuda(err, "routing scan kernel");
   }
-  err = launch_mx_dispatch(dtype, x, T, d, E, k, rb, topk_idx, lrank, blk_cnt, offsets, mtile, topk_gate, inv, rgate,
-                           xq, xq_sc, status, stream);
+  md.topk_idx = topk_idx;
+  md.topk_gate = topk_gate;
+  md.lrank = lrank;
+  md.blk = blk_cnt;
+  md.counts = cnt;
+  md.offsets = offsets;
+  md.mtile = mtile;
+  err = launch_mx_dispatch(dtype, x, T, d, E, k, md, inv, rgate, xq, xq_sc, status, stream);
   if (err != cudaSuccess) return fail_cuda(err, "dispatch kernel");
   MxOut hid = {};
   hid.h = h;
@@ -164,10 +181,12 @@ moe_status mx_layer(const void* x, const void* w_router, const float* b_router, 
   if (err != cudaSuccess) return fail_cuda(err, "gate/up product (MXFP4)");
   MxOut yo = {};
   yo.out = y;
+  yo.form = kMxY16;
+  yo.y_exp = ws + l.y_exp;
   yo.gate = rgate;
   err = launch_mx_product(down, offsets, E, R, d, I, (int)mx_group_tiles(d), yo, status, stream);
   if (err != cudaSuccess) return fail_cuda(err, "down product (MXFP4)");
-  err = launch_mx_combine(y, inv, T, d, k, out, status, stream);
+  err = launch_mx_combine(y, ws + l.y_exp, inv, T, d, k, out, status, stream);
   if (err != cudaSuccess) return fail_cuda(err, "combine kernel");
   return MOE_OK;
 }
@@ -260,7 +279,7 @@ moe_status moe_mx_matmul(const void* a, const void* a_scales, const void* b, con
     return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed (driver entry point unavailable or bad pointer)");
   MxOut o = {};
   o.out = out;
-  o.f32 = out_dtype == MOE_F32;
+  o.form = out_dtype == MOE_F32 ? kMxF32 : kMxBf16;
   const cudaError_t err = launch_mx_product(m, offsets, groups, M, N, K, (int)mx_group_tiles(N), o, status_dev,
                                             static_cast<cudaStream_t>(stream));
   return err == cudaSuccess ? MOE_OK : fail_cuda(err, "MXFP4 product kernel");

@@ -369,7 +369,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
               *reinterpret_cast<const uint32_t*>(sc + lane * 16);
       } else {
         const float gs = out.gate && first + lane < t.cnt ? out.gate[t.row0 + first + lane] : 1.f;
-        const int el = out.f32 ? 4 : 2;
+        const int el = out.form == kMxF32 ? 4 : 2;
         const int cols = 64 / el;  // of a pass
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
@@ -393,7 +393,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
             }
           }
         };
-        if (out.f32) {
+        if (out.form == kMxF32) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const uint32_t* w = &v[c >> 1][(c & 1) * 16];
@@ -404,9 +404,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             uint32_t w[16];
+            uint32_t e = 0xffu;
+            if (out.form == kMxY16) {
+              uint32_t m = 0;
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              w[i] = pack_bf16x2(__uint_as_float(v[c][2 * i]), __uint_as_float(v[c][2 * i + 1]));
+              for (int i = 0; i < 32; ++i) m = max(m, v[c][i] & 0x7fffffffu);
+              e = y16_exp(m);
+              const int col = t.n * 256 + part * 64 + c * 32;
+              if (first + lane < t.cnt && col < N)
+                out.y_exp[y16_exp_at((size_t)M, col, (size_t)(t.row0 + first + lane))] = (uint8_t)e;
+            }
+            const float inv = y16_inv(e);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float x = __uint_as_float(v[c][2 * i]), y = __uint_as_float(v[c][2 * i + 1]);
+              w[i] = e == 0xffu ? pack_bf16x2(x, y) : y16_pack(x, y, inv);
+            }
             pass(c * 32, make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7]),
                  make_uint4(w[8], w[9], w[10], w[11]), make_uint4(w[12], w[13], w[14], w[15]));
           }

@@ -28,12 +28,15 @@ struct MxMaps {
   CUtensorMap a, sa, b0, b1, sb0, sb1;
 };
 
-// Where an MXFP4 product writes: out [M, N] fp32 or bf16, each row multiplied
-// by gate[row] (NULL: 1), or for gate/up the MXFP4 hidden rows.
+// Where an MXFP4 product writes: out [M, N] in bf16, fp32 or, each row
+// multiplied by gate[row], as 16-bit numbers with their exponents in y_exp
+// (mx.cuh, y16); or for gate/up the MXFP4 hidden rows.
+enum MxForm { kMxBf16, kMxF32, kMxY16 };
 struct MxOut {
   void* out;
-  int f32;
+  int form;
   const float* gate;
+  uint8_t* y_exp;
   uint8_t* h;
   uint8_t* h_scales;
 };
@@ -60,16 +63,32 @@ bool make_tmap_mx_scales(CUtensorMap* map, const void* base, uint64_t rows);
 cudaError_t launch_mx_count(const int32_t* topk_idx, int T, int E, int k, int32_t* lrank, int32_t* blk_cnt,
                             float* blk_psum, int32_t* status, cudaStream_t stream);
 
+// How the dispatch gets the rows of the experts: from the routing scan's
+// results (blk_base, offsets and mtile), from the counts of each block of rb
+// tokens, or from the choices themselves. In the last two cases it writes
+// counts, offsets and mtile.
+enum MxScan { kScanDone, kScanBlocks, kScanAll };
+// At most this many choices are counted by every block of the dispatch (1.3 us
+// for 4096), and this many counts of token blocks summed by each; more take
+// kernels of their own.
+constexpr int kScanAllMost = 4096, kScanBlocksMost = 8192;
+struct MxDispatch {
+  MxScan scan;
+  int rb;
+  const int32_t* topk_idx;
+  const float* topk_gate;
+  const int32_t* lrank;    // [T, k] rank among the token block's choices of the expert (not for kScanAll)
+  const int32_t* blk;      // [nb, E] base rows (kScanDone) or counts (kScanBlocks)
+  int32_t *counts, *offsets, *mtile;
+};
 // Each token's row of x to MXFP4 once, written at the row of each of its
-// choices (base row of its block and expert plus its rank); also inv [T, k]
-// (-1 for a choice out of range) and the rows' gates.
-cudaError_t launch_mx_dispatch(moe_dtype dtype, const void* x, int T, int d, int E, int k, int rb,
-                               const int32_t* topk_idx, const int32_t* lrank, const int32_t* blk_base,
-                               const int32_t* offsets, const int32_t* mtile, const float* topk_gate, int32_t* inv,
-                               float* rgate, void* data, void* scales, int32_t* status, cudaStream_t stream);
+// choices; also inv [T, k] (-1 for a choice out of range) and the rows' gates.
+cudaError_t launch_mx_dispatch(moe_dtype dtype, const void* x, int T, int d, int E, int k, const MxDispatch& a,
+                               int32_t* inv, float* rgate, void* data, void* scales, int32_t* status,
+                               cudaStream_t stream);
 
-// out[t] = sum over t's choices of the rows Y[inv[t, j]] (bf16, gated already).
-cudaError_t launch_mx_combine(const void* y, const int32_t* inv, int T, int d, int k, void* out, int32_t* status,
-                              cudaStream_t stream);
+// out[t] = sum over t's choices of the rows Y[inv[t, j]] (y16, gated already).
+cudaError_t launch_mx_combine(const void* y, const uint8_t* y_exp, const int32_t* inv, int T, int d, int k, void* out,
+                              int32_t* status, cudaStream_t stream);
 
 }  // namespace moe

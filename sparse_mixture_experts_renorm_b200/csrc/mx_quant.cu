@@ -113,98 +113,6 @@ struct Pieces {
   }
 };
 
-// 32 bytes to or from memory that is used once, a whole sector at once where
-// the address allows (rows are multiples of 32 bytes, so `wide` is a question
-// of the first one's).
-__device__ __forceinline__ void load_sector(uint32_t (&w)[8], const void* p, bool wide) {
-  if (wide) {
-    asm volatile("ld.global.cs.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
-                 : "l"(p));
-  } else {
-    const uint4 a = __ldcs(static_cast<const uint4*>(p)), b = __ldcs(static_cast<const uint4*>(p) + 1);
-    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
-  }
-}
-__device__ __forceinline__ void store_sector(void* p, const uint32_t (&w)[8], bool wide) {
-  if (wide) {
-    asm volatile("st.global.cs.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]),
-                 "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                 : "memory");
-  } else {
-    __stcs(static_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
-    __stcs(static_cast<uint4*>(p) + 1, make_uint4(w[4], w[5], w[6], w[7]));
-  }
-}
-
-// A piece in registers: 16 bf16 or 8 fp32, and its codes.
-template <typename T>
-struct Piece;
-template <>
-struct Piece<__nv_bfloat16> {
-  static constexpr int kCols = 16;
-  using Codes = uint2;
-  uint32_t w[8];
-  // The largest magnitude's bits as those of a float.
-  __device__ __forceinline__ uint32_t amax() const {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
-    return max(m << 16, m & 0xffff0000u);
-  }
-  // Times a power of two: exact where it is not so small that its code is 0.
-  __device__ __forceinline__ Codes codes(float inv) const {
-    const __nv_bfloat162 s = __float2bfloat162_rn(inv);
-    float q[16];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const __nv_bfloat162 t = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]), s);
-      const uint32_t b = *reinterpret_cast<const uint32_t*>(&t);
-      q[2 * i] = __uint_as_float(b << 16);
-      q[2 * i + 1] = __uint_as_float(b & 0xffff0000u);
-    }
-    return make_uint2(mx_pack8(q), mx_pack8(q + 8));
-  }
-  __device__ __forceinline__ void values(const Codes& c, float scale) {
-    const __nv_bfloat162 s = __float2bfloat162_rn(scale);
-    uint32_t a[4], b[4];
-    mx_values8(c.x, a);
-    mx_values8(c.y, b);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const __nv_bfloat162 t = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(i < 4 ? &a[i] : &b[i - 4]), s);
-      w[i] = *reinterpret_cast<const uint32_t*>(&t);
-    }
-  }
-};
-template <>
-struct Piece<float> {
-  static constexpr int kCols = 8;
-  using Codes = uint32_t;
-  uint32_t w[8];
-  __device__ __forceinline__ uint32_t amax() const {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, w[i] & 0x7fffffffu);
-    return m;
-  }
-  __device__ __forceinline__ Codes codes(float inv) const {
-    float q[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = __uint_as_float(w[i]) * inv;
-    return mx_pack8(q);
-  }
-  __device__ __forceinline__ void values(const Codes& c, float s) {
-    uint32_t a[4];
-    mx_values8(c, a);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      w[2 * i] = __float_as_uint(__uint_as_float(a[i] << 16) * s);
-      w[2 * i + 1] = __float_as_uint(__uint_as_float(a[i] & 0xffff0000u) * s);
-    }
-  }
-};
-
 // The first piece of this lane.
 __device__ __forceinline__ unsigned long long first_piece() {
   return ((unsigned long long)blockIdx.x * (kQThreads / 32) + (threadIdx.x >> 5)) * (kQUnits * 32) + (threadIdx.x & 31);
