@@ -49,7 +49,7 @@ constexpr int kSfBytes = 3 * kMxStageBytes;     // scales of 128 rows, and of 25
 constexpr int kOutPitch = 80;
 constexpr int kOutWarp = 32 * kOutPitch;
 constexpr int kMxSmem = kMxStages * (2 * kHalf + kSfBytes) + kMxEpiWarps * kOutWarp + 1024 + 4096;
-constexpr uint32_t kStageTx = 2u * (2 * kHalf + kSfBytes);  // both CTAs
+constexpr uint32_t kStageTx = 2u * (2 * kHalf + kSfBytes);  // both CTAs, all rows
 constexpr uint32_t kSfCol = 256;                // first TMEM column of the scales
 constexpr int kSfBufs = 4, kSfCols = 32;
 static_assert(kMxSmem <= 227 * 1024, "shared memory");
@@ -224,15 +224,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
         const CUtensorMap* mB = kGateUp && rank ? &tmB1 : &tmB0;
         const int bsf0 = (t.g * group_tiles + (kGateUp ? t.n : 2 * t.n)) * KB;
         const int bsf1 = kGateUp ? bsf0 : bsf0 + KB;
+        // the second CTA's rows, if there are any (its part of the tile is then
+        // what an earlier one left, and nobody takes the products)
+        const bool second = t.m * 256 + 128 < t.cnt;
+        const bool load_a = leader || second;
+        const uint32_t tx = kStageTx - (second ? 0u : (uint32_t)kHalf);
         for (int kb = 0; kb < KB; ++kb) {
           if (!mbar_wait(&empty[stage], phase ^ 1u, s_abort, status, limit_ns)) {
             ok = false;
             break;
           }
           const uint32_t fbar = map_to_cta(&full[stage], 0);
-          if (leader) mbar_arrive_expect_tx(&full[stage], kStageTx);
+          if (leader) mbar_arrive_expect_tx(&full[stage], tx);
           uint8_t* ss = sS + stage * kSfBytes;
-          tma_load_2d_pair(sA + stage * kHalf, &tmA, fbar, kb * 128, arow);
+          if (load_a) tma_load_2d_pair(sA + stage * kHalf, &tmA, fbar, kb * 128, arow);
           tma_load_2d_pair(sB + stage * kHalf, mB, fbar, kb * 128, brow);
           tma_load_2d_pair(ss, &tmSA, fbar, 0, asf + kb);
           tma_load_2d_pair(ss + kMxStageBytes, &tmSB0, fbar, 0, bsf0 + kb);
@@ -268,8 +273,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
       int buf = 0;
       bool ok = true;
       for (int tile = cid; ok && tile < total; tile += ncl) {
-        if (!mbar_wait(tempty, acc_phase ^ 1u, s_abort, status, limit_ns)) break;
-        tc_fence_after();
         for (int kb = 0; kb < KB; ++kb) {
           if (!mbar_wait(&full[stage], phase, s_abort, status, limit_ns)) {
             ok = false;
@@ -287,6 +290,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
             tc_cp_scales_pair(sf + 4 * t, scales_desc(ss + 512 * t));
             tc_cp_scales_pair(sf + 8 + 8 * t, scales_desc(ss + kMxStageBytes + 512 * t));
             tc_cp_scales_pair(sf + 12 + 8 * t, scales_desc(ss + 2 * kMxStageBytes + 512 * t));
+          }
+          if (kb == 0) {  // the accumulator; the scales did not have to wait for it
+            if (!mbar_wait(tempty, acc_phase ^ 1u, s_abort, status, limit_ns)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
           }
           const uint64_t adesc = sw128_kmajor_desc(smem_u32(sA + stage * kHalf));
           const uint64_t bdesc = sw128_kmajor_desc(smem_u32(sB + stage * kHalf));
