@@ -24,6 +24,7 @@ __global__ void __launch_bounds__(kCountThreads) mx_count_kernel(const int32_t* 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int i = threadIdx.x; i < kCountWarps * kMaxExperts; i += kCountThreads) (&s_cnt[0][0])[i] = 0;
   pdl_wait();
+  pdl_trigger();
   __syncthreads();
   const long long base = (long long)blockIdx.x * kRouterTokensTc * k;
   const int n = (int)min((long long)kRouterTokensTc * k, (long long)T * k - base);
@@ -155,6 +156,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) mx_dispatch_kernel(const X* __
   const int t0 = blockIdx.x * kTok, nt = min(kTok, T - t0);
   const int per = d / kCols, pieces = nt * per;  // of a token, of the block (whose rows are contiguous)
   pdl_wait();
+  pdl_trigger();
   const bool wide = (reinterpret_cast<uintptr_t>(x) & 31) == 0;
   const X* src = x + (size_t)t0 * d;
   Piece<X> v[kDispatchPieces];
@@ -257,6 +259,7 @@ __global__ void __launch_bounds__(kRowThreads) mx_combine_kernel(const uint4* __
   __shared__ int row[kMaxTopK];
   const int R = T * k, t = blockIdx.x;
   pdl_wait();
+  pdl_trigger();
   if (threadIdx.x < kMaxTopK) {
     int r = (int)threadIdx.x < k ? inv[(size_t)t * k + threadIdx.x] : -1;
     if (r >= R) {

@@ -173,6 +173,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
     tmem_relinquish_pair();
   }
   pdl_wait();
+  pdl_trigger();
   __syncthreads();
   // the groups' rows and the prefix of their 256-row tiles
   for (int i = threadIdx.x; i <= G; i += blockDim.x) {
@@ -438,7 +439,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
     }
   }
 
-  pdl_trigger();
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // no CTA leaves while its peer may still touch its shared memory or TMEM
@@ -449,12 +449,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
   }
 }
 
-// Resident CTA pairs per GPU, queried once per device and kernel.
+// Resident CTA pairs per GPU, queried once per device and kernel (which is
+// given its shared memory then).
 int max_pairs(const void* kern, std::atomic<int>* cache) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
   const int have = cache[dev].load(std::memory_order_acquire);
   if (have > 0) return have;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMxSmem) != cudaSuccess) return 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2, 1, 1);
   cfg.blockDim = dim3(kMxThreads, 1, 1);
@@ -477,8 +479,6 @@ cudaError_t launch(const MxMaps& m, const int32_t* offsets, int G, int M, int N,
                    const MxOut& out, int32_t* status, cudaStream_t stream) {
   static std::atomic<int> cache[64];
   auto kern = mx_gemm_kernel<kGateUp>;
-  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMxSmem);
-  if (err != cudaSuccess) return err;
   const int pairs = max_pairs(reinterpret_cast<const void*>(kern), cache);
   if (pairs <= 0) return cudaErrorInvalidConfiguration;
   const long long n_wb = kGateUp ? (N + 127) / 128 : (N + 255) / 256;

@@ -126,6 +126,7 @@ __global__ void __launch_bounds__(kQThreads) mx_quantize_kernel(const T* __restr
                                                                 uint8_t* __restrict__ scales) {
   __shared__ Groups s_g;
   pdl_wait();
+  pdl_trigger();
   if (offsets) load_groups(s_g, offsets, G);
   const int st = mx_stages(cols);
   const unsigned long long u = first_piece();
@@ -170,6 +171,7 @@ __global__ void __launch_bounds__(kQThreads) mx_dequantize_kernel(const uint8_t*
                                                                   T* __restrict__ out) {
   __shared__ Groups s_g;
   pdl_wait();
+  pdl_trigger();
   if (offsets) load_groups(s_g, offsets, G);
   const int st = mx_stages(cols);
   const unsigned long long u = first_piece();

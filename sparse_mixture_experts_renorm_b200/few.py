@@ -10,7 +10,7 @@ from . import _binding as B
 from ._call import check, cuda, device_status, dtype_code, need, on, ptr
 
 
-@dataclass
+@dataclass(slots=True)
 class FewOutputs:
     out: torch.Tensor  # [T, d] in x's dtype
     topk_idx: torch.Tensor  # [T, k] int32
@@ -66,18 +66,19 @@ def moe_forward_few(x, w_router, b_router, w_gate, w_up, w_down, k: int, renorm:
         else:
             need("workspace", workspace, torch.uint8, None, dev)
         if out is None:
-            out = torch.empty((T, d), dtype=dt, device=dev)
+            out = torch.empty_like(x)
         else:
             need("out", out, dt, (T, d), dev)
         if topk_idx is None:
-            topk_idx = torch.empty((T, k), dtype=torch.int32, device=dev)
+            topk_idx = torch.empty_strided((T, k), (k, 1), dtype=torch.int32, device=dev)
         else:
             need("topk_idx", topk_idx, torch.int32, (T, k), dev)
         if topk_gate is None:
-            topk_gate = torch.empty((T, k), dtype=torch.float32, device=dev)
+            topk_gate = torch.empty_strided((T, k), (k, 1), dtype=torch.float32, device=dev)
         else:
             need("topk_gate", topk_gate, torch.float32, (T, k), dev)
-        check(lib.moe_forward_few(ptr(x), ptr(w_router), ptr(b_router), ptr(w_gate), ptr(w_up), ptr(w_down), T, d, E,
-                                  k, I, int(bool(renorm)), code, ptr(out), ptr(topk_idx), ptr(topk_gate), ptr(counts),
-                                  ptr(aux), ptr(workspace), workspace.numel(), ptr(status), s), lib)
+        check(lib.moe_forward_few(x.data_ptr(), w_router.data_ptr(), ptr(b_router), w_gate.data_ptr(),
+                                  w_up.data_ptr(), w_down.data_ptr(), T, d, E, k, I, 1 if renorm else 0, code,
+                                  out.data_ptr(), topk_idx.data_ptr(), topk_gate.data_ptr(), ptr(counts), ptr(aux),
+                                  workspace.data_ptr(), workspace.numel(), status.data_ptr(), s), lib)
     return FewOutputs(out, topk_idx, topk_gate, status, counts, aux)

@@ -14,7 +14,7 @@ from ._call import check, cuda, device_status, dtype_code, need, on, ptr
 _BYTE = torch.uint8
 
 
-@dataclass
+@dataclass(slots=True)
 class MXTensor:
     """An MXFP4 matrix or stack of matrices: ``data`` [rows, cols / 2] or
     [groups, rows, cols / 2] uint8 (two E2M1 codes a byte, the even column in
@@ -74,8 +74,8 @@ def mx_quantize(x, offsets=None, *, stream=None) -> MXTensor:
     off, groups = _offsets(offsets, dev) if offsets is not None else (None, x.shape[0] if x.dim() == 3 else 1)
     with on(dev, stream) as s:
         n = mx_scale_bytes(groups, rows, cols, offsets is not None)
-        data = torch.empty((*x.shape[:-1], cols // 2), dtype=_BYTE, device=dev)
-        scales = torch.empty((n,), dtype=_BYTE, device=dev)
+        data = x.new_empty((*x.shape[:-1], cols // 2), dtype=_BYTE)
+        scales = x.new_empty((n,), dtype=_BYTE)
         check(lib.moe_mx_quantize(ptr(x), off, groups, rows, cols, dt, ptr(data), ptr(scales), n, s), lib)
     return MXTensor(data, scales)
 
@@ -89,15 +89,18 @@ def mx_dequantize(q: MXTensor, dtype=torch.bfloat16, offsets=None, *, out=None, 
     dev = cuda("q.data", q.data)
     _check_mx("q", q, dev)
     dt = dtype_code(dtype)
-    if offsets is not None and q.data.dim() != 2:
+    shape = q.data.shape
+    if offsets is not None and len(shape) != 2:
         raise ValueError("a matrix with offsets is [rows, cols]")
     lib = B.load_library()
-    rows, cols = q.shape[-2], q.shape[-1]
-    off, groups = _offsets(offsets, dev) if offsets is not None else (None, q.shape[0] if q.data.dim() == 3 else 1)
+    rows, cols = shape[-2], 2 * shape[-1]
+    shape = (*shape[:-1], cols)
+    off, groups = _offsets(offsets, dev) if offsets is not None else (None, shape[0] if len(shape) == 3 else 1)
     with on(dev, stream) as s:
         if out is None:
-            out = torch.empty(q.shape, dtype=dtype, device=dev)
-        need("out", out, dtype, q.shape, dev)
+            out = q.data.new_empty(shape, dtype=dtype)
+        else:
+            need("out", out, dtype, shape, dev)
         check(lib.moe_mx_dequantize(ptr(q.data), ptr(q.scales), q.scales.numel(), off, groups, rows, cols, dt,
                                     ptr(out), s), lib)
     return out
@@ -117,18 +120,19 @@ def mx_matmul(a: MXTensor, b: MXTensor, offsets=None, *, out_dtype=torch.bfloat1
     _check_mx("a", a, dev)
     _check_mx("b", b, dev)
     dt = dtype_code(out_dtype)
-    groups = b.data.shape[0] if b.data.dim() == 3 else 1
-    N, K = b.shape[-2], b.shape[-1]
-    M = a.shape[-2]
+    sa, sb = a.data.shape, b.data.shape
+    groups = sb[0] if len(sb) == 3 else 1
+    N, K = sb[-2], 2 * sb[-1]
+    M = sa[-2]
     off = None
     if offsets is not None:
         off, n = _offsets(offsets, dev)
-        if a.data.dim() != 2 or n != groups:
+        if len(sa) != 2 or n != groups:
             raise ValueError(f"with offsets a is [M, K] and there are as many groups as in b ({groups})")
-    elif (a.data.shape[0] if a.data.dim() == 3 else 1) != groups:
+    elif (sa[0] if len(sa) == 3 else 1) != groups:
         raise ValueError("without offsets a and b have the same number of groups")
-    if a.shape[-1] != K:
-        raise ValueError(f"a has {a.shape[-1]} columns and b {K}")
+    if 2 * sa[-1] != K:
+        raise ValueError(f"a has {2 * sa[-1]} columns and b {K}")
     lib = B.load_library()
     for name, q, g, rows, ragged in (("a", a, groups, M, off is not None), ("b", b, groups, N, False)):
         n = mx_scale_bytes(g, rows, K, ragged)
@@ -136,18 +140,20 @@ def mx_matmul(a: MXTensor, b: MXTensor, offsets=None, *, out_dtype=torch.bfloat1
             raise ValueError(f"{name}.scales holds {q.scales.numel()} bytes, {n} are needed")
     if status is None:
         status = device_status(dev)
-    need("status", status, torch.int32, (1,), dev)
-    shape = (*a.data.shape[:-1], N)
+    else:
+        need("status", status, torch.int32, (1,), dev)
+    shape = (*sa[:-1], N)
     with on(dev, stream) as s:
         if out is None:
-            out = torch.empty(shape, dtype=out_dtype, device=dev)
-        need("out", out, out_dtype, shape, dev)
+            out = a.data.new_empty(shape, dtype=out_dtype)
+        else:
+            need("out", out, out_dtype, shape, dev)
         check(lib.moe_mx_matmul(ptr(a.data), ptr(a.scales), ptr(b.data), ptr(b.scales), off, groups, M, N, K, dt,
                                 ptr(out), ptr(status), s), lib)
     return out
 
 
-@dataclass
+@dataclass(slots=True)
 class MXOutputs:
     out: torch.Tensor  # [T, d] bf16
     counts: torch.Tensor  # [E] int32
@@ -172,33 +178,35 @@ def _weights(w_gate, w_up, w_down, dev, d):
         _check_mx(name, q, dev)
         if q.data.dim() != 3:
             raise ValueError(f"{name} must be [E, rows, cols]")
-    E, I, _ = w_gate.shape
-    for name, q, shape in (("w_gate", w_gate, (E, I, d)), ("w_up", w_up, (E, I, d)), ("w_down", w_down, (E, d, I))):
-        if tuple(q.shape) != shape:
+    E, I, _ = w_gate.data.shape
+    n_up, n_down = mx_scale_bytes(E, I, d), mx_scale_bytes(E, d, I)
+    for name, q, shape, n in (("w_gate", w_gate, (E, I, d), n_up), ("w_up", w_up, (E, I, d), n_up),
+                              ("w_down", w_down, (E, d, I), n_down)):
+        got = q.data.shape
+        if got[0] != shape[0] or got[1] != shape[1] or 2 * got[2] != shape[2]:
             raise ValueError(f"{name} must have the shape {shape} (got {tuple(q.shape)})")
-        n = mx_scale_bytes(*shape)
         if q.scales.numel() < n:
             raise ValueError(f"{name}.scales holds {q.scales.numel()} bytes, {n} are needed")
-    w = B.moe_mx_weights()
-    w.struct_bytes = ctypes.sizeof(B.moe_mx_weights)
-    w.gate, w.gate_scales = w_gate.data.data_ptr(), w_gate.scales.data_ptr()
-    w.up, w.up_scales = w_up.data.data_ptr(), w_up.scales.data_ptr()
-    w.down, w.down_scales = w_down.data.data_ptr(), w_down.scales.data_ptr()
+    w = B.moe_mx_weights(ctypes.sizeof(B.moe_mx_weights), w_gate.data.data_ptr(), w_gate.scales.data_ptr(),
+                         w_up.data.data_ptr(), w_up.scales.data_ptr(), w_down.data.data_ptr(),
+                         w_down.scales.data_ptr())
     return w, E, I
 
 
 def _buffers(x, T, d, E, k, I, out, counts, workspace, status):
     dev = x.device
     if out is None:
-        out = torch.empty((T, d), dtype=torch.bfloat16, device=dev)
-    need("out", out, torch.bfloat16, (T, d), dev)
+        out = x.new_empty((T, d), dtype=torch.bfloat16)
+    else:
+        need("out", out, torch.bfloat16, (T, d), dev)
     if counts is None:
-        counts = torch.empty((E,), dtype=torch.int32, device=dev)
-    need("counts", counts, torch.int32, (E,), dev)
-    size = mx_workspace_size(T, d, E, k, I)
+        counts = x.new_empty((E,), dtype=torch.int32)
+    else:
+        need("counts", counts, torch.int32, (E,), dev)
     if workspace is None:
-        workspace = torch.empty((size,), dtype=_BYTE, device=dev)
-    need("workspace", workspace, _BYTE, None, dev)
+        workspace = x.new_empty((mx_workspace_size(T, d, E, k, I),), dtype=_BYTE)
+    else:  # its size is checked by the call
+        need("workspace", workspace, _BYTE, None, dev)
     if status is not None:
         need("status", status, torch.int32, (1,), dev)
     return out, counts, workspace
