@@ -436,8 +436,8 @@ moe_status moe_mx_matmul(const void* a, const void* a_scales, const void* b, con
  * The layer with its experts in MXFP4: x is rounded to MXFP4 row by row (the
  * router sees x itself), both products of an expert multiply MXFP4 matrices,
  * and the SwiGLU hidden rows are rounded to MXFP4 from fp32 between them. Each
- * expert row times its gate is kept to 2^-14 of the largest of its 32 columns
- * (rounded to nearest), a token's rows are added in slot order in fp32, and out
+ * expert row times its gate is rounded to 2^-11 of a value (2^-25 of the
+ * largest of its 32 columns where that is more), a token's rows are added in slot order in fp32, and out
  * [T, d] is bf16. d % 32 == 0 and I % 32 == 0.
  *
  * moe_mx_experts takes the choices and gates: topk_idx [T, k], any experts

@@ -2,6 +2,8 @@
 // E8M0 scale): the layout of the scales and the rounding of one block.
 #pragma once
 
+#include <cuda_fp16.h>
+
 #include "common.cuh"
 
 namespace moe {
@@ -171,29 +173,22 @@ struct Piece<float> {
 };
 
 // Rows of expert outputs between the down product and the sum over a token's
-// experts: 16-bit whole numbers with one exponent byte per 32 columns, 2^13 to
-// 2^14 for the largest of them, which leaves 2^-14 of it where bf16 would leave
-// 2^-8 of each value: half the error of the whole layer, for the same bytes.
-// exponent byte 0xFF: the block holds a NaN or an infinity, and the columns are
-// bf16. Exponent bytes stand by 256 columns and rows, eight for each.
+// experts: fp16 with one exponent byte per 32 columns, by which the largest of
+// them lies in [1, 2). That leaves 2^-11 of a value where bf16 would leave
+// 2^-8, half the error of the whole layer, for the same bytes. Exponent byte
+// 0xFF: the block holds a NaN or an infinity, and its columns are bf16.
+// Exponent bytes stand by 256 columns and rows, eight for each.
 __host__ __device__ __forceinline__ size_t y16_exp_at(size_t rows, int col, size_t row) {
   return ((size_t)(col >> 8) * rows + row) * 8 + ((col >> 5) & 7);
 }
-__device__ __forceinline__ uint32_t y16_exp(uint32_t amax_bits) { return max(amax_bits >> 23, 16u); }
-// v * 2^(13 - E) as a whole number in the low 16 bits (E = exponent - 127).
+__device__ __forceinline__ uint32_t y16_exp(uint32_t amax_bits) { return max(amax_bits >> 23, 1u); }
+__device__ __forceinline__ float y16_inv(uint32_t e) { return __uint_as_float((254u - e) << 23); }  // 2^(127 - e)
+__device__ __forceinline__ float y16_step(uint32_t e) { return __uint_as_float(e << 23); }          // 2^(e - 127)
 __device__ __forceinline__ uint32_t y16_pack(float a, float b, float inv) {
-  // adding 1.5 * 2^23 rounds to a whole number and leaves it in the low bits
-  const uint32_t x = __float_as_uint(fmaf(a, inv, 12582912.f)), y = __float_as_uint(fmaf(b, inv, 12582912.f));
-  return __byte_perm(x, y, 0x5410);
+  const __half2 h = __floats2half2_rn(a * inv, b * inv);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ float y16_inv(uint32_t e) { return __uint_as_float((267u - e) << 23); }   // 2^(140 - e)
-__device__ __forceinline__ float y16_step(uint32_t e) { return __uint_as_float((e - 13u) << 23); }   // 2^(e - 140)
-// The two whole numbers of a word (times y16_step they are the values).
-__device__ __forceinline__ float2 y16_numbers(uint32_t w) {
-  const uint32_t u = w ^ 0x80008000u;  // biased by 32768
-  const float lo = __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7610)) - 8421376.f;
-  const float hi = __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7632)) - 8421376.f;
-  return make_float2(lo, hi);
-}
+// The two numbers of a word (times y16_step they are the values).
+__device__ __forceinline__ float2 y16_numbers(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
 
 }  // namespace moe

@@ -150,9 +150,10 @@ __global__ void __launch_bounds__(kRowThreads, 4) mx_dispatch_kernel(const X* __
   constexpr int kCols = Piece<X>::kCols, kLanes = 32 / kCols;  // lanes of a block of 32 columns
   static_assert(kTok == 1 || kTok * kMaxTopK <= kRowThreads, "a thread per choice");
   __shared__ DispatchPlan s_p;
-  __shared__ int s_row[kTok * kMaxTopK];   // dispatched row, -1: none
-  __shared__ int s_tile[kTok * kMaxTopK];  // tile row of its scales
-  __shared__ int s_in[kTok * kMaxTopK];    // row in the tile
+  // where a choice's codes and scales begin; NULL: nowhere
+  __shared__ uint8_t* s_data[kTok * kMaxTopK];
+  __shared__ uint8_t* s_scale[kTok * kMaxTopK];
+  const int st = mx_stages(d);
   const int t0 = blockIdx.x * kTok, nt = min(kTok, T - t0);
   const int per = d / kCols, pieces = nt * per;  // of a token, of the block (whose rows are contiguous)
   pdl_wait();
@@ -195,16 +196,14 @@ __global__ void __launch_bounds__(kRowThreads, 4) mx_dispatch_kernel(const X* __
         atomicOr(status, MOE_DEV_INTERNAL);
         row = -1;
       } else {
-        s_tile[o] = 2 * tile + (in >> 7);
-        s_in[o] = in & 127;
+        s_scale[o] = scales + mx_scale_at((size_t)(2 * tile + (in >> 7)), st, in & 127, 0);
         rgate[row] = gate;
       }
     }
-    s_row[o] = row;
+    s_data[o] = row >= 0 ? data + (size_t)row * (d / 2) : nullptr;
     inv[oi] = row;
   }
   __syncthreads();
-  const int st = mx_stages(d);
   const bool words = d % 128 == 0;  // four blocks' bytes are then a word, and 4 kLanes lanes of one row hold them
   for (int p0 = 0; p0 < pieces; p0 += kDispatchPieces * kRowThreads) {
     if (p0 > 0) {
@@ -230,20 +229,23 @@ __global__ void __launch_bounds__(kRowThreads, 4) mx_dispatch_kernel(const X* __
       if (!have) continue;
       const typename Piece<X>::Codes code = v[i].codes(mx_inv_scale(sb));
       const int t = kTok == 1 ? 0 : p / per, q = p - t * per, b = q / kLanes;
-      for (int j = 0; j < k; ++j) {
-        const int o = t * k + j;
-        if (s_row[o] < 0) continue;
-        *reinterpret_cast<typename Piece<X>::Codes*>(data + (size_t)s_row[o] * (d / 2) + (size_t)q * (kCols / 2)) = code;
+      const int at = (b >> 3) * kMxStageBytes + ((b >> 2) & 1) * 512 + (b & 3);  // from the row's first scale
+      const bool stores = words ? q % (4 * kLanes) == 0 : q % kLanes == 0;
+      const bool ends = b == d / 32 - (words ? 4 : 1);  // zeros follow to the end of the stage
+#pragma unroll 2
+      for (int o = t * k; o < t * k + k; ++o) {
+        uint8_t* to = s_data[o];
+        if (!to) continue;
+        *reinterpret_cast<typename Piece<X>::Codes*>(to + q * (kCols / 2)) = code;
+        if (!stores) continue;
+        to = s_scale[o];
         if (words) {
-          if (q % (4 * kLanes) == 0) {
-            uint8_t* to = scales + mx_scale_at((size_t)s_tile[o], st, s_in[o], b);
-            *reinterpret_cast<uint32_t*>(to) = word;
-            if (b == d / 32 - 4 && (b & 4) == 0) *reinterpret_cast<uint32_t*>(to + 512) = 0;  // behind the row's last
-          }
-        } else if (q % kLanes == 0) {
-          scales[mx_scale_at((size_t)s_tile[o], st, s_in[o], b)] = (uint8_t)sb;
-          if (b == d / 32 - 1)  // zeros behind the row's last
-            for (int z = b + 1; z < 8 * st; ++z) scales[mx_scale_at((size_t)s_tile[o], st, s_in[o], z)] = 0;
+          *reinterpret_cast<uint32_t*>(to + at) = word;
+          if (ends && (b & 4) == 0) *reinterpret_cast<uint32_t*>(to + at + 512) = 0;
+        } else {
+          to[at] = (uint8_t)sb;
+          if (ends)
+            for (int z = b + 1; z < 8 * st; ++z) to[(z >> 3) * kMxStageBytes + ((z >> 2) & 1) * 512 + (z & 3)] = 0;
         }
       }
     }
@@ -271,6 +273,7 @@ __global__ void __launch_bounds__(kRowThreads) mx_combine_kernel(const uint4* __
   __syncthreads();
   const int i = blockIdx.y * kRowThreads + threadIdx.x;
   if (i >= nvec) return;
+  const uint8_t* exps = y_exp + y16_exp_at((size_t)R, i * 8, 0);
   constexpr int kAtOnce = 4;  // rows in flight: more take registers that other blocks need
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
@@ -282,7 +285,7 @@ __global__ void __launch_bounds__(kRowThreads) mx_combine_kernel(const uint4* __
       const int r = row[j0 + j];
       if (r >= 0) {
         v[j] = __ldg(y + (size_t)r * nvec + i);
-        e[j] = __ldg(y_exp + y16_exp_at((size_t)R, i * 8, (size_t)r));
+        e[j] = __ldg(exps + (size_t)r * 8);
       }
     }
 #pragma unroll

@@ -194,8 +194,9 @@ def experts64(xv, idx, gate, wg, wu, wd, dims):
     the product of the two, plus 2^-18 of the value for the fp32 exponential,
     division and products. What that can move behind the rounding to MXFP4 is
     found by rounding both ends with both scales that the block can get. Then
-    the down product's own error, each gated row's rounding (half a step of
-    2^-13 of the largest of 32 columns, no less than 2^-126), and the sum's."""
+    the down product's own error, each gated row's rounding (fp16, 2^-11 of the
+    value or, below its normal numbers, 2^-25 of the largest of 32 columns), and
+    the sum's."""
     T, d, I, k = dims
     out, tol = np.zeros((T, d)), np.zeros((T, d))
     for t in range(T):
@@ -218,7 +219,7 @@ def experts64(xv, idx, gate, wg, wu, wd, dims):
             dy = np.abs(wd[e]) @ move + I * 2.0**-23 * (np.abs(wd[e]) @ (np.abs(q) + move))
             out[t] += gate[t, j] * y
             top = np.pad(np.abs(gate[t, j] * y) + np.abs(gate[t, j]) * dy, (0, -d % 32)).reshape(-1, 32).max(1)
-            tol[t] += np.abs(gate[t, j]) * (dy + 2.0**-23 * np.abs(y)) + 2.0**-14 * 1.01 * np.repeat(top, 32)[:d] + 2.0**-126
+            tol[t] += np.abs(gate[t, j]) * (dy + 2.0**-23 * np.abs(y)) + 2.0**-11 * 1.01 * np.abs(gate[t, j]) * (np.abs(y) + dy) + 2.0**-25 * np.repeat(top, 32)[:d] + 2.0**-126
     return out, tol + 2.0**-8 * (np.abs(out) + tol) + 2.0**-120
 
 
