@@ -16,7 +16,8 @@
 // columns of K: 128 bytes of codes a row with the 128-byte swizzle, as for 64
 // bf16, and 1024 bytes of scales per 128 rows, which one thread copies to TMEM
 // (tcgen05.cp) in front of the stage's four UMMAs. Both CTAs need the scales
-// of all 256 weight rows. 35 KB a stage, 5 stages. The issuing thread is the
+// of all 256 weight rows. 35 KB a stage, 6 stages (a load's round trip is 1.4 us
+// and a stage's products take 0.28: five stages run dry). The issuing thread is the
 // one that elect.sync names: the compiler then keeps the operands in uniform
 // registers. With a test of the lane it moved them there in front of every
 // instruction, 99 cycles for a copy and 135 for a product, and a stage took
@@ -39,16 +40,12 @@
 namespace moe {
 namespace {
 
-constexpr int kMxStages = 5;
+constexpr int kMxStages = 6;
 constexpr int kMxEpiWarps = 16;
 constexpr int kMxThreads = 64 + 32 * kMxEpiWarps;
 constexpr int kHalf = 128 * 128;                // 128 rows x 256 codes
 constexpr int kSfBytes = 3 * kMxStageBytes;     // scales of 128 rows, and of 256 weight rows
-// Results pass through shared memory on their way out: 64 bytes of each of a
-// warp's 32 rows, 80 apart so that eight rows' 16 bytes fall on all banks.
-constexpr int kOutPitch = 80;
-constexpr int kOutWarp = 32 * kOutPitch;
-constexpr int kMxSmem = kMxStages * (2 * kHalf + kSfBytes) + kMxEpiWarps * kOutWarp + 1024 + 4096;
+constexpr int kMxSmem = kMxStages * (2 * kHalf + kSfBytes) + 1024 + 4096;
 constexpr uint32_t kStageTx = 2u * (2 * kHalf + kSfBytes);  // both CTAs, all rows
 constexpr uint32_t kSfCol = 256;                // first TMEM column of the scales
 constexpr int kSfBufs = 4, kSfCols = 32;
@@ -92,8 +89,29 @@ __device__ __forceinline__ uint64_t scales_desc(uint32_t smem_addr) {
   return desc;
 }
 
-// A barrier of the four epilogue warps of one lane quarter.
-__device__ __forceinline__ void quarter_sync(int q) { asm volatile("bar.sync %0, 128;" ::"r"(1 + q) : "memory"); }
+// Four lanes, each with four 16-byte units of its own row: lane l of the four
+// gets unit l of every one of their rows, so that a store of the warp writes
+// 64 consecutive bytes of eight rows.
+__device__ __forceinline__ void transpose_units(uint32_t (&w)[4][4]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    const int o = 1 << s;
+    const bool up = lane & o;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (u & o) continue;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? w[u][i] : w[u + o][i], o);
+        if (up)
+          w[u][i] = got;
+        else
+          w[u + o][i] = got;
+      }
+    }
+  }
+}
 
 struct MxTile {
   int g, m, n, row0, cnt;  // group, 256-row tile, weight block, first row and rows of the group
@@ -135,8 +153,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
   uint8_t* sA = smem;
   uint8_t* sB = smem + kMxStages * kHalf;
   uint8_t* sS = smem + 2 * kMxStages * kHalf;
-  uint8_t* sOut = smem + kMxStages * (2 * kHalf + kSfBytes);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sOut + kMxEpiWarps * kOutWarp);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kMxStages * (2 * kHalf + kSfBytes));
   uint64_t* full = bars;               // leader: the stage's bytes of both CTAs
   uint64_t* empty = bars + kMxStages;  // both: stage consumed by the pair's UMMAs
   uint64_t* tfull = bars + 2 * kMxStages;
@@ -328,7 +345,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
     // TMEM lane = a row of this CTA's half of the tile. The four groups of
     // four warps take 64 columns each, or 32 units of the gate and up halves.
     const int q = warp & 3, part = (warp - 2) >> 2;
-    uint8_t* mine = sOut + (warp - 2) * kOutWarp;
     const uint32_t tempty_leader = map_to_cta(tempty, 0);
     const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
     uint32_t acc_phase = 0;
@@ -347,7 +363,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster_cta(tempty_leader);
       const int first = t.m * 256 + (int)rank * 128 + q * 32;  // this warp's first row in its group
-      if (first >= t.cnt) continue;  // none of them exists (the other parts of the quarter leave as well)
+      if (first >= t.cnt) continue;  // none of them exists
       if (kGateUp) {
         const int unit0 = t.n * 128 + part * 32;
         float h[32];
@@ -361,60 +377,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
         const float inv = mx_inv_scale(sb);
 #pragma unroll
         for (int i = 0; i < 32; ++i) h[i] *= inv;
-        // the quarter's four parts side by side: 64 bytes of codes and four of
-        // scales a row
-        uint8_t* rows = sOut + q * (32 * kOutPitch);
-        uint8_t* sc = sOut + 4 * (32 * kOutPitch) + q * 4;
-        quarter_sync(q);
-        *reinterpret_cast<uint4*>(rows + lane * kOutPitch + part * 16) =
-            make_uint4(mx_pack8(h), mx_pack8(h + 8), mx_pack8(h + 16), mx_pack8(h + 24));
-        sc[lane * 16 + part] = (uint8_t)sb;
-        quarter_sync(q);
-        const int r = part * 8 + (lane >> 2), at = t.n * 64 + (lane & 3) * 16;
-        if (first + r < t.cnt && at < N / 2)
-          *reinterpret_cast<uint4*>(out.h + (size_t)(t.row0 + first + r) * (N / 2) + at) =
-              *reinterpret_cast<const uint4*>(rows + r * kOutPitch + (lane & 3) * 16);
-        if (part == 0)
-          *reinterpret_cast<uint32_t*>(out.h_scales + mx_scale_at((size_t)(2 * (s_mt[t.g] + t.m) + (int)rank), mx_stages(N),
-                                                                 rt, t.n * 4)) =
-              *reinterpret_cast<const uint32_t*>(sc + lane * 16);
+        if (first + lane < t.cnt) {
+          if (unit0 < N)
+            *reinterpret_cast<uint4*>(out.h + (size_t)(t.row0 + first + lane) * (N / 2) + unit0 / 2) =
+                make_uint4(mx_pack8(h), mx_pack8(h + 8), mx_pack8(h + 16), mx_pack8(h + 24));
+          // one of the four bytes of this row in the block's tile of scales
+          out.h_scales[mx_scale_at((size_t)(2 * (s_mt[t.g] + t.m) + (int)rank), mx_stages(N), rt, t.n * 4 + part)] =
+              (uint8_t)sb;
+        }
       } else {
-        const float gs = out.gate && first + lane < t.cnt ? out.gate[t.row0 + first + lane] : 1.f;
         const int el = out.form == kMxF32 ? 4 : 2;
         const int cols = 64 / el;  // of a pass
+        if (out.form == kMxY16) {
+          const float gs = first + lane < t.cnt ? out.gate[t.row0 + first + lane] : 0.f;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
+          for (int c = 0; c < 2; ++c)
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[c][i] = __float_as_uint(gs * __uint_as_float(v[c][i]));
+            for (int i = 0; i < 32; ++i) v[c][i] = __float_as_uint(gs * __uint_as_float(v[c][i]));
         }
-        auto pass = [&](int c0, const uint4& a, const uint4& b, const uint4& d, const uint4& e) {
-          __syncwarp();
-          uint4* w = reinterpret_cast<uint4*>(mine + lane * kOutPitch);
-          w[0] = a, w[1] = b, w[2] = d, w[3] = e;
-          __syncwarp();
-          const int col = t.n * 256 + part * 64 + c0 + (lane & 3) * (cols / 4);
-          uint8_t* dst = static_cast<uint8_t*>(out.out) + ((size_t)(t.row0 + first) * N + col) * el;
+        // 64 bytes of every row, from column c0 of this warp's 64
+        auto pass = [&](int c0, uint32_t (&w)[4][4]) {
+          transpose_units(w);
+          const int col = t.n * 256 + part * 64 + c0 + (lane & 3) * (cols / 4), r0 = lane & ~3;
+          uint8_t* dst = static_cast<uint8_t*>(out.out) + ((size_t)(t.row0 + first + r0) * N + col) * el;
           if (col < N) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int r = i * 8 + (lane >> 2);
-              if (first + r < t.cnt)
-                *reinterpret_cast<uint4*>(dst + (size_t)r * N * el) =
-                    *reinterpret_cast<const uint4*>(mine + r * kOutPitch + (lane & 3) * 16);
-            }
+            for (int r = 0; r < 4; ++r)
+              if (first + r0 + r < t.cnt)
+                *reinterpret_cast<uint4*>(dst + (size_t)r * N * el) = make_uint4(w[r][0], w[r][1], w[r][2], w[r][3]);
           }
         };
         if (out.form == kMxF32) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            const uint32_t* w = &v[c >> 1][(c & 1) * 16];
-            pass(c * 16, make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7]),
-                 make_uint4(w[8], w[9], w[10], w[11]), make_uint4(w[12], w[13], w[14], w[15]));
+            uint32_t w[4][4];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i >> 2][i & 3] = v[c >> 1][(c & 1) * 16 + i];
+            pass(c * 16, w);
           }
         } else {
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            uint32_t w[16];
+            uint32_t w[4][4];
             uint32_t e = 0xffu;
             if (out.form == kMxY16) {
               uint32_t m = 0;
@@ -429,10 +433,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               const float x = __uint_as_float(v[c][2 * i]), y = __uint_as_float(v[c][2 * i + 1]);
-              w[i] = e == 0xffu ? pack_bf16x2(x, y) : y16_pack(x, y, inv);
+              w[i >> 2][i & 3] = e == 0xffu ? pack_bf16x2(x, y) : y16_pack(x, y, inv);
             }
-            pass(c * 32, make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7]),
-                 make_uint4(w[8], w[9], w[10], w[11]), make_uint4(w[12], w[13], w[14], w[15]));
+            pass(c * 32, w);
           }
         }
       }
