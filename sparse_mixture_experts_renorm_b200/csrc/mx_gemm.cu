@@ -285,10 +285,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
   } else if (warp == 1) {
     // ------------------------------------------ MMA issuer (leader only) --
     if (leader && elect_one()) {
+      // few instructions a stage: the epilogue's warps share this warp's
+      // scheduler, and while they compute the products wait for this one
+      const uint64_t a0 = sw128_kmajor_desc(smem_u32(sA)), b0 = sw128_kmajor_desc(smem_u32(sB));
+      const uint64_t s0 = scales_desc(smem_u32(sS));
+      const int whole = K / kMxStageCols;  // stages of four steps of 64 columns; the last may have fewer
       int stage = 0;
       uint32_t phase = 0;
       uint32_t acc_phase = 0;
-      int buf = 0;
+      uint32_t sf = tmem_base + kSfCol;
+      uint64_t adesc = a0, bdesc = b0, sdesc = s0;
       bool ok = true;
       for (int tile = cid; ok && tile < total; tile += ncl) {
         for (int kb = 0; kb < KB; ++kb) {
@@ -297,17 +303,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
             break;
           }
           tc_fence_after();
-          const uint32_t ss = smem_u32(sS + stage * kSfBytes);
-          const uint32_t sf = tmem_base + kSfCol + static_cast<uint32_t>(buf * kSfCols);
-          const int steps = min(4, (K - kb * kMxStageCols + 63) >> 6);  // 64 columns each
           // columns: A's two tiles at 0 and 4, B's two at 8 and 16 (eight
-          // columns: the scales of 2 x 128 weight rows)
+          // columns: the scales of 2 x 128 weight rows). A short last stage's
+          // second half is copied too and not used.
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
-            if (2 * t >= steps) break;
-            tc_cp_scales_pair(sf + 4 * t, scales_desc(ss + 512 * t));
-            tc_cp_scales_pair(sf + 8 + 8 * t, scales_desc(ss + kMxStageBytes + 512 * t));
-            tc_cp_scales_pair(sf + 12 + 8 * t, scales_desc(ss + 2 * kMxStageBytes + 512 * t));
+            tc_cp_scales_pair(sf + 4 * t, sdesc + (512 >> 4) * t);
+            tc_cp_scales_pair(sf + 8 + 8 * t, sdesc + (kMxStageBytes >> 4) + (512 >> 4) * t);
+            tc_cp_scales_pair(sf + 12 + 8 * t, sdesc + (2 * kMxStageBytes >> 4) + (512 >> 4) * t);
           }
           if (kb == 0) {  // the accumulator; the scales did not have to wait for it
             if (!mbar_wait(tempty, acc_phase ^ 1u, s_abort, status, limit_ns)) {
@@ -316,20 +319,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
             }
             tc_fence_after();
           }
-          const uint64_t adesc = sw128_kmajor_desc(smem_u32(sA + stage * kHalf));
-          const uint64_t bdesc = sw128_kmajor_desc(smem_u32(sB + stage * kHalf));
+          if (kb < whole) {
 #pragma unroll
-          for (int s = 0; s < 4; ++s) {
-            if (s >= steps) break;
-            tc_mma_mxf4_pair(tmem_base, adesc + static_cast<uint64_t>(s * 2), bdesc + static_cast<uint64_t>(s * 2),
-                             idesc_mxf4(256, 256, s & 1 ? 2u : 0u), sf + 4 * (s >> 1), sf + 8 + 8 * (s >> 1),
-                             (kb | s) != 0 ? 1u : 0u);
+            for (int s = 0; s < 4; ++s)
+              tc_mma_mxf4_pair(tmem_base, adesc + 2 * s, bdesc + 2 * s, idesc_mxf4(256, 256, s & 1 ? 2u : 0u),
+                               sf + 4 * (s >> 1), sf + 8 + 8 * (s >> 1), s > 0 ? 1u : (uint32_t)kb);
+          } else {
+            const int steps = (K - kb * kMxStageCols + 63) >> 6;
+#pragma unroll 1
+            for (int s = 0; s < steps; ++s)
+              tc_mma_mxf4_pair(tmem_base, adesc + 2 * s, bdesc + 2 * s, idesc_mxf4(256, 256, s & 1 ? 2u : 0u),
+                               sf + 4 * (s >> 1), sf + 8 + 8 * (s >> 1), (uint32_t)(kb | s));
           }
           tc_commit_pair_both(&empty[stage]);
-          buf = (buf + 1) & (kSfBufs - 1);
+          sf = sf == tmem_base + kSfCol + (kSfBufs - 1) * kSfCols ? tmem_base + kSfCol : sf + kSfCols;
+          adesc += kHalf >> 4;
+          bdesc += kHalf >> 4;
+          sdesc += kSfBytes >> 4;
           if (++stage == kMxStages) {
             stage = 0;
             phase ^= 1u;
+            adesc = a0, bdesc = b0, sdesc = s0;
           }
         }
         if (!ok) break;
