@@ -55,6 +55,7 @@ constexpr int kSmemTotal = 227 * 1024;
 struct Plan {
   int n_act;                        // experts with tokens
   int most;                         // tokens of the one with most
+  int down_split;                   // parts of a down product's columns
   int expert[kMaxRows];             // ascending
   int base[kMaxRows + 1];           // first row of each
   int tj[kMaxRows];                 // t * k + j of a row
@@ -119,14 +120,21 @@ struct Ring {
   int slot, stages, groups;
 };
 template <typename X, bool kUp>
-__device__ __forceinline__ Ring ring_of(uint8_t* base, const Plan& p, int group) {
-  constexpr int kBytes = kSmemTotal - fixed_bytes<X>();
-  int rows = kUp ? p.most : p.most * Traits<X>::kHid;
+__device__ __forceinline__ int ring_slot(int most) {
+  int rows = kUp ? most : most * Traits<X>::kHid;
   if (sizeof(X) == 4) rows = (rows + 3) & ~3;  // fp32 multiplies four token rows at a time
+  return (kWeightBytes + rows * kTokPitch + 127) & ~127;
+}
+template <typename X>
+__device__ __forceinline__ int ring_groups(int slot) {
+  return Traits<X>::kGroups == 2 && 6 * slot <= kSmemTotal - fixed_bytes<X>() ? 2 : 1;
+}
+template <typename X, bool kUp>
+__device__ __forceinline__ Ring ring_of(uint8_t* base, const Plan& p, int group) {
   Ring r;
-  r.slot = (kWeightBytes + rows * kTokPitch + 127) & ~127;
-  r.groups = Traits<X>::kGroups == 2 && 6 * r.slot <= kBytes ? 2 : 1;
-  r.stages = min(kMaxStages, kBytes / (r.groups * r.slot));
+  r.slot = ring_slot<X, kUp>(p.most);
+  r.groups = ring_groups<X>(r.slot);
+  r.stages = min(kMaxStages, (kSmemTotal - fixed_bytes<X>()) / (r.groups * r.slot));
   r.base = base + (size_t)group * r.stages * r.slot;
   return r;
 }
@@ -196,8 +204,9 @@ __device__ __forceinline__ float reduce_many(float (&v)[N]) {
 
 // Groups the choices by expert: idx[T * k] in shared memory, every thread of
 // the block. A token names an expert once.
-__device__ void make_plan(Plan& p, const int* idx, const float* gate, int T, int E, int k) {
-  const int R = T * k;
+template <typename X>
+__device__ void make_plan(const FewArgs& a, Plan& p, const int* idx, const float* gate) {
+  const int E = a.E, k = a.k, R = a.T * k;
   for (int e = threadIdx.x; e < E; e += blockDim.x) p.mask[e] = 0;
   __syncthreads();
   const int i = threadIdx.x;
@@ -226,10 +235,23 @@ __device__ void make_plan(Plan& p, const int* idx, const float* gate, int T, int
       act += __popc(live);
       rows += __shfl_sync(0xffffffffu, incl, 31);
     }
+    // lane q - 1: the busiest group's work if columns are split in q parts. An
+    // item's own overhead (its sums, its join) is some two chunks; a finer
+    // split has to gain 3 %
+    const int chunks = (a.I * (int)sizeof(X) + kChunk - 1) / kChunk, q = lane + 1;
+    const int units = a.down_blocks * ring_groups<X>(ring_slot<X, false>(most));
+    float t = 3.0e38f;
+    if (q <= min(a.split, chunks))
+      t = (float)((act * ((a.d + kRows - 1) / kRows) * q + units - 1) / units) * (float)((chunks + q - 1) / q + 2);
+    float least = t;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) least = fminf(least, __shfl_xor_sync(0xffffffffu, least, o));
+    const int split = __ffs(__ballot_sync(0xffffffffu, t <= 1.03f * least));
     if (lane == 0) {
       p.n_act = act;
       p.most = most;
       p.base[act] = rows;
+      p.down_split = split;
     }
   }
   __syncthreads();
@@ -445,23 +467,11 @@ struct Item {
 template <typename X, bool kUp>
 struct Work {
   int n_blk, split, chunks, total;
-  // units: groups of all blocks
-  __device__ Work(const FewArgs& a, int n_act, int units) {
-    const int K = kUp ? a.d : a.I;
-    chunks = (K * (int)sizeof(X) + kChunk - 1) / kChunk;
-    n_blk = kUp ? (a.I + 7) / 8 : (a.d + 15) / 16;
-    split = 1;
-    const int items = n_act * n_blk;
-    if (!kUp) {
-      // the parts that leave the busiest group the least to do; an item's own
-      // overhead (its sums, its join) is some two chunks
-      float best = 3.0e38f;
-      for (int q = 1; q <= min(a.split, chunks); ++q) {
-        const float t = (float)((items * q + units - 1) / units) * (float)((chunks + q - 1) / q + 2);
-        if (t < 0.97f * best) best = t, split = q;
-      }
-    }
-    total = items * split;
+  __device__ __forceinline__ Work(const FewArgs& a, int n_act, int parts) {
+    chunks = ((kUp ? a.d : a.I) * (int)sizeof(X) + kChunk - 1) / kChunk;
+    n_blk = kUp ? (a.I + 7) / 8 : (a.d + kRows - 1) / kRows;
+    split = parts;
+    total = n_act * n_blk * split;
   }
   __device__ __forceinline__ Item item(int i) const {
     Item w;
@@ -501,9 +511,9 @@ __device__ __forceinline__ size_t hidden_at(int first, int n, int chunks, int ch
 
 // Asks for the weights of block `block`'s first stages to be brought to L2.
 template <typename X, bool kUp>
-__device__ void prefetch_weights(const FewMaps& maps, const FewArgs& a, const int* expert, int n_act, int block,
-                                 int grid, int units) {
-  const Work<X, kUp> work(a, n_act, units);
+__device__ void prefetch_weights(const FewMaps& maps, const FewArgs& a, const int* expert, int n_act, int split,
+                                 int block, int grid) {
+  const Work<X, kUp> work(a, n_act, split);
   const int row_bytes = (kUp ? a.d : a.I) * (int)sizeof(X);
   int n = 0;
   for (int i = block; i < work.total; i += grid) {
@@ -553,7 +563,7 @@ __device__ __forceinline__ void load_weights(const FewMaps& maps, uint8_t* dst, 
 template <typename X>
 __device__ bool produce_up_weights(const FewMaps& maps, const FewArgs& a, Ctrl& c, Group& g, const Ring& ring, int first,
                                    int step, Pos& pos, int& issued) {
-  const Work<X, true> work(a, c.plan.n_act, step);
+  const Work<X, true> work(a, c.plan.n_act, 1);
   const int row_bytes = a.d * (int)sizeof(X);
   for (int i = first; i < work.total; i += step) {
     const Item w = work.item(i);
@@ -574,7 +584,7 @@ template <typename X>
 __device__ bool produce_up_tokens(const FewArgs& a, Ctrl& c, Group& g, const Ring& ring, int first, int step, Pos& pos,
                                   int& issued) {
   const int lane = threadIdx.x & 31;
-  const Work<X, true> work(a, c.plan.n_act, step);
+  const Work<X, true> work(a, c.plan.n_act, 1);
   const int row_bytes = a.d * (int)sizeof(X);
   for (int i = first; i < work.total; i += step) {
     const Item w = work.item(i, c.plan);
@@ -604,7 +614,7 @@ __device__ bool produce_up_tokens(const FewArgs& a, Ctrl& c, Group& g, const Rin
 template <typename X>
 __device__ bool produce_down(const FewMaps& maps, const FewArgs& a, Ctrl& c, Group& g, const Ring& ring, int first,
                              int step, Pos& pos, int& issued) {
-  const Work<X, false> work(a, c.plan.n_act, step);
+  const Work<X, false> work(a, c.plan.n_act, c.plan.down_split);
   const int row_bytes = a.I * (int)sizeof(X);
   const int own = 1 + ring.stages * work.split / work.chunks;
   int i = first;
@@ -793,7 +803,7 @@ __device__ __forceinline__ float sum_parts(const float* red, int row, int n) {
 template <typename X>
 __device__ void consume_up(const FewArgs& a, Ctrl& c, Group& g, const Ring& ring, float* red2, int group, int first,
                            int step) {
-  const Work<X, true> work(a, c.plan.n_act, step);
+  const Work<X, true> work(a, c.plan.n_act, 1);
   const int hid_chunks = (a.I * (int)sizeof(X) + kChunk - 1) / kChunk;
   const int tid = threadIdx.x - (group * kGroupWarps + 2) * 32;
   Pos pos;
@@ -893,8 +903,8 @@ __device__ void join(const FewArgs& a, Ctrl& c, Group& g, const Work<X, false>& 
 
 // few_down's products.
 template <typename X>
-__device__ void consume_down(const FewArgs& a, Ctrl& c, Group& g, const Ring& ring, float* red2, int group, int step) {
-  const Work<X, false> work(a, c.plan.n_act, step);
+__device__ void consume_down(const FewArgs& a, Ctrl& c, Group& g, const Ring& ring, float* red2, int group) {
+  const Work<X, false> work(a, c.plan.n_act, c.plan.down_split);
   const int tid = threadIdx.x - (group * kGroupWarps + 2) * 32;
   const int R = a.T * a.k;
   Pos pos;
@@ -945,8 +955,8 @@ __device__ void stream(const FewMaps& maps, const FewArgs& a, Ctrl& c, uint8_t* 
         ok = produce_down<X>(maps, a, c, g, ring, first, step, pos, issued);
       // few_down's first stages, while this kernel ends and that one starts
       if (kUp && ok && group == 0)
-        prefetch_weights<X, false>(maps, a, c.plan.expert, c.plan.n_act, blockIdx.x, a.down_blocks,
-                                   a.down_blocks * ring_of<X, false>(smem_ring, c.plan, 0).groups);
+        prefetch_weights<X, false>(maps, a, c.plan.expert, c.plan.n_act, c.plan.down_split, blockIdx.x,
+                                   a.down_blocks);
       if (!ok || c.abort) drain(a, g, ring, pos, issued);
     }
     __syncwarp();
@@ -956,14 +966,14 @@ __device__ void stream(const FewMaps& maps, const FewArgs& a, Ctrl& c, uint8_t* 
       if (lane == 0 && (!ok || c.abort)) drain(a, g, ring, pos, issued);
       __syncwarp();
     } else {
-      join<X>(a, c, g, Work<X, false>(a, c.plan.n_act, step));
+      join<X>(a, c, g, Work<X, false>(a, c.plan.n_act, c.plan.down_split));
     }
   } else {
     red += group * 2 * red_floats<X>();
     if constexpr (kUp)
       consume_up<X>(a, c, g, ring, red, group, first, step);
     else
-      consume_down<X>(a, c, g, ring, red, group, step);
+      consume_down<X>(a, c, g, ring, red, group);
   }
 }
 
@@ -997,7 +1007,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(threads<X>(),
   uint8_t* ring;
   carve<X>(smem, &c, &red, &ring);
   init_ctrl<X, true>(*c);
-  if (a.likely && threadIdx.x == 32) prefetch_weights<X, true>(maps, a, nullptr, a.E, blockIdx.x, gridDim.x, gridDim.x);
+  if (a.likely && threadIdx.x == 32) prefetch_weights<X, true>(maps, a, nullptr, a.E, 1, blockIdx.x, gridDim.x);
   float* part = reinterpret_cast<float*>(ring);                     // [kCluster][T][E]
   float* scratch = part + (size_t)kCluster * a.T * a.E;             // [kWarps][16][kPassLd]
   const int rank = (int)cluster_ctarank();
@@ -1018,7 +1028,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(threads<X>(),
   const bool first = blockIdx.x == 0;
   choose(a, part, reinterpret_cast<uint32_t*>(scratch), *c, first);
   __syncthreads();
-  make_plan(c->plan, c->idx, c->gate, a.T, a.E, a.k);
+  make_plan<X>(a, c->plan, c->idx, c->gate);
   if (first && (a.counts || a.aux)) statistics(a, part, *c);
   fence_async();  // the ring's memory was written above, and is next by the copies
   __syncthreads();
@@ -1046,7 +1056,7 @@ __global__ void __launch_bounds__(threads<X>(), 1) few_down_kernel(const __grid_
     c->gate[i] = a.gate[i];
   }
   __syncthreads();
-  make_plan(c->plan, c->idx, c->gate, a.T, a.E, a.k);
+  make_plan<X>(a, c->plan, c->idx, c->gate);
   fence_async();  // few_up's hidden rows are read by the copies
   stream<X, false>(maps, a, *c, ring, red);
 }
