@@ -208,3 +208,36 @@ def test_two_streams_at_once_and_a_graph():
         torch.cuda.synchronize()
         assert torch.equal(out, moe_forward_few(**dict(p, x=p["x"] * scale), k=2, renorm=True).out)
     assert int(device_status("cuda").item()) == 0
+
+
+def test_tokens_and_output_at_an_odd_multiple_of_16_bytes():
+    p = layer(5, 136, 6, 2, 200, 11, BF16)
+    want = moe_forward_few(**p, k=2, renorm=True).out
+    x = torch.empty((8 + 5 * 136,), dtype=BF16, device="cuda")[8:].view(5, 136)
+    x.copy_(p["x"])
+    out = torch.full((8 + 5 * 136 + 8,), 7.0, dtype=BF16, device="cuda")
+    r = moe_forward_few(**dict(p, x=x), k=2, renorm=True, out=out[8:-8].view(5, 136))
+    assert x.data_ptr() % 32 == 16 and torch.equal(r.out, want)
+    assert (out[:8] == 7).all() and (out[-8:] == 7).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_weights_of_experts_that_nobody_chose_are_not_read(dtype):
+    p = layer(8, 128, 10, 2, 64, 12, dtype)
+    p["b_router"] = torch.tensor([0, 9, 0, 0, 9, 0, 0, 0, 0, 0.0], device="cuda") * 10
+    want = moe_forward_few(**p, k=2, renorm=True).out.clone()
+    for n in ("w_gate", "w_up", "w_down"):
+        for e in (0, 2, 3, 5, 6, 7, 8, 9):
+            p[n][e] = float("nan")
+    assert torch.equal(moe_forward_few(**p, k=2, renorm=True).out, want)
+
+
+def test_hidden_units_and_columns_that_end_inside_a_block():
+    # the rows behind an expert's last are the next expert's, or none
+    for dtype, d, I in ((BF16, 24, 8), (F32, 20, 4), (F32, 12, 28)):
+        p = layer(3, d, 2, 2, I, 13, dtype)
+        p["w_gate"][1], p["w_up"][1], p["w_down"][1] = (p[n][1] * 1e4 for n in ("w_gate", "w_up", "w_down"))
+        p["b_router"] = torch.tensor([0.0, -200.0], device="cuda")  # the second expert's gate is 0
+        r = moe_forward_few(**p, k=1, renorm=True)
+        assert (r.topk_idx == 0).all()
+        check_out(p, r.topk_idx, r.topk_gate, r.out, dtype)
