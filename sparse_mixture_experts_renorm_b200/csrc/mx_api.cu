@@ -66,6 +66,10 @@ moe_status check_mx_shape(int T, int d, int E, int k, int I) {
   return MOE_OK;
 }
 
+bool row_maps(MxMaps* m, const void* a, uint64_t rows, uint64_t row_bytes) {
+  return make_tmap_mx_codes(&m->a, a, rows, row_bytes) && make_tmap_mx_codes(&m->a32, a, rows, row_bytes, 32);
+}
+
 bool weight_maps(MxMaps* m, const void* b0, const void* s0, const void* b1, const void* s1, uint64_t E, uint64_t N,
                  uint64_t K) {
   const uint64_t rows = E * (uint64_t)mx_group_tiles((long long)N) * mx_stage_count((int)K);
@@ -125,10 +129,10 @@ moe_status mx_layer(const void* x, const void* w_router, const float* b_router, 
   uint8_t *xq = ws + l.xq, *xq_sc = ws + l.xq_sc, *h = ws + l.h, *h_sc = ws + l.h_sc, *y = ws + l.y;
 
   MxMaps up, down;
-  if (!make_tmap_mx_codes(&up.a, xq, (uint64_t)R, (uint64_t)d / 2) ||
+  if (!row_maps(&up, xq, (uint64_t)R, (uint64_t)d / 2) ||
       !make_tmap_mx_scales(&up.sa, xq_sc, (uint64_t)l.tiles * mx_stage_count(d)) ||
       !weight_maps(&up, w->gate, w->gate_scales, w->up, w->up_scales, E, I, d) ||
-      !make_tmap_mx_codes(&down.a, h, (uint64_t)R, (uint64_t)I / 2) ||
+      !row_maps(&down, h, (uint64_t)R, (uint64_t)I / 2) ||
       !make_tmap_mx_scales(&down.sa, h_sc, (uint64_t)l.tiles * mx_stage_count(I)) ||
       !weight_maps(&down, w->down, w->down_scales, w->down, w->down_scales, E, d, I))
     return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed (driver entry point unavailable or bad pointer)");
@@ -273,7 +277,7 @@ moe_status moe_mx_matmul(const void* a, const void* a_scales, const void* b, con
   if (!aligned16(a) || !aligned16(a_scales) || !aligned16(b) || !aligned16(b_scales) || !aligned16(out))
     return fail(MOE_ERR_INVALID_ARG, "codes, scales and out must be 16-byte aligned");
   MxMaps m;
-  if (!make_tmap_mx_codes(&m.a, a, (offsets ? 1ull : (uint64_t)groups) * M, (uint64_t)K / 2) ||
+  if (!row_maps(&m, a, (offsets ? 1ull : (uint64_t)groups) * M, (uint64_t)K / 2) ||
       !make_tmap_mx_scales(&m.sa, a_scales, (uint64_t)a_tiles * stages) ||
       !weight_maps(&m, b, b_scales, b, b_scales, groups, N, K))
     return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed (driver entry point unavailable or bad pointer)");

@@ -143,7 +143,8 @@ __device__ __forceinline__ MxTile mx_tile(int tile, int n_wb, const int* s_off, 
 // product tmB1/tmSB1 repeat tmB0/tmSB0.
 template <bool kGateUp>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
-    mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmSA,
+    mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA32,
+                   const __grid_constant__ CUtensorMap tmSA,
                    const __grid_constant__ CUtensorMap tmB0, const __grid_constant__ CUtensorMap tmB1,
                    const __grid_constant__ CUtensorMap tmSB0, const __grid_constant__ CUtensorMap tmSB1,
                    const int32_t* __restrict__ offsets, int G, int M, int N, int K, int group_tiles,
@@ -189,6 +190,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
     tmem_alloc_pair(s_tmem, 512);
     tmem_relinquish_pair();
   }
+  // Rows that a group lacks are not loaded. The tensor cores multiply what is
+  // there all the same, with most of the power if it is data: zeros.
+  for (int i = threadIdx.x; i < kMxStages * kHalf / 16; i += kMxThreads)
+    reinterpret_cast<uint4*>(sA)[i] = make_uint4(0, 0, 0, 0);
+  asm volatile("fence.proxy.async;" ::: "memory");
   pdl_wait();
   pdl_trigger();
   __syncthreads();
@@ -242,11 +248,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
         const CUtensorMap* mB = kGateUp && rank ? &tmB1 : &tmB0;
         const int bsf0 = (t.g * group_tiles + (kGateUp ? t.n : 2 * t.n)) * KB;
         const int bsf1 = kGateUp ? bsf0 : bsf0 + KB;
-        // the second CTA's rows, if there are any (its part of the tile is then
-        // what an earlier one left, and nobody takes the products)
-        const bool second = t.m * 256 + 128 < t.cnt;
-        const bool load_a = leader || second;
-        const uint32_t tx = kStageTx - (second ? 0u : (uint32_t)kHalf);
+        // this CTA's rows that exist, in boxes of 32, and the other's
+        const int rows = t.cnt - t.m * 256;
+        const int boxes0 = min(4, (rows + 31) >> 5), boxes1 = max(0, min(4, (rows - 128 + 31) >> 5));
+        const int boxes = leader ? boxes0 : boxes1;
+        const uint32_t tx = kStageTx - (uint32_t)((8 - boxes0 - boxes1) * (kHalf / 4));
         for (int kb = 0; kb < KB; ++kb) {
           if (!mbar_wait(&empty[stage], phase ^ 1u, s_abort, status, limit_ns)) {
             ok = false;
@@ -255,7 +261,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
           const uint32_t fbar = map_to_cta(&full[stage], 0);
           if (leader) mbar_arrive_expect_tx(&full[stage], tx);
           uint8_t* ss = sS + stage * kSfBytes;
-          if (load_a) tma_load_2d_pair(sA + stage * kHalf, &tmA, fbar, kb * 128, arow);
+          if (boxes == 4) {
+            tma_load_2d_pair(sA + stage * kHalf, &tmA, fbar, kb * 128, arow);
+          } else {
+            for (int b = 0; b < boxes; ++b)
+              tma_load_2d_pair(sA + stage * kHalf + b * (kHalf / 4), &tmA32, fbar, kb * 128, arow + 32 * b);
+          }
           tma_load_2d_pair(sB + stage * kHalf, mB, fbar, kb * 128, brow);
           tma_load_2d_pair(ss, &tmSA, fbar, 0, asf + kb);
           tma_load_2d_pair(ss + kMxStageBytes, &tmSB0, fbar, 0, bsf0 + kb);
@@ -499,7 +510,7 @@ cudaError_t launch(const MxMaps& m, const int32_t* offsets, int G, int M, int N,
   const long long most = row_tiles * n_wb;
   const int clusters = (int)(most < pairs ? most : pairs);
   if (clusters <= 0) return cudaSuccess;
-  return launch_pdl(kern, dim3(2 * clusters), dim3(kMxThreads), kMxSmem, stream, m.a, m.sa, m.b0, m.b1, m.sb0, m.sb1,
+  return launch_pdl(kern, dim3(2 * clusters), dim3(kMxThreads), kMxSmem, stream, m.a, m.a32, m.sa, m.b0, m.b1, m.sb0, m.sb1,
                     offsets, G, M, N, K, group_tiles, out, status, kWaitLimitNs);
 }
 

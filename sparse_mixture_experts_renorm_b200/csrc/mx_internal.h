@@ -22,10 +22,10 @@ cudaError_t launch_mx_dequantize(moe_dtype dtype, const void* data, const void* 
                                  int cols, const int32_t* offsets, int G, int group_tiles, size_t tile_rows, void* out,
                                  cudaStream_t stream);
 
-// Tensor maps of one MXFP4 product: codes and scales of A, and of one or two
-// weights (the product repeats the first).
+// Tensor maps of one MXFP4 product: codes of A in boxes of 128 and of 32 rows,
+// its scales, and those of one or two weights (the product repeats the first).
 struct MxMaps {
-  CUtensorMap a, sa, b0, b1, sb0, sb1;
+  CUtensorMap a, a32, sa, b0, b1, sb0, sb1;
 };
 
 // Where an MXFP4 product writes: out [M, N] in bf16, fp32 or, each row
@@ -50,9 +50,9 @@ cudaError_t launch_mx_product(const MxMaps& m, const int32_t* offsets, int G, in
 cudaError_t launch_mx_gateup(const MxMaps& m, const int32_t* offsets, int G, int M, int N, int K, int group_tiles,
                              const MxOut& out, int32_t* status, cudaStream_t stream);
 
-// Codes [rows, row_bytes] in boxes of 128 rows x 128 bytes (128-byte swizzle),
+// Codes [rows, row_bytes] in boxes of box_rows x 128 bytes (128-byte swizzle),
 // and scales as rows of 1024 bytes, one row a box. False on failure.
-bool make_tmap_mx_codes(CUtensorMap* map, const void* base, uint64_t rows, uint64_t row_bytes);
+bool make_tmap_mx_codes(CUtensorMap* map, const void* base, uint64_t rows, uint64_t row_bytes, uint32_t box_rows = 128);
 bool make_tmap_mx_scales(CUtensorMap* map, const void* base, uint64_t rows);
 
 // The dispatch of given choices: per block of kRouterTokensTc tokens the
