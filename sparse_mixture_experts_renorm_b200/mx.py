@@ -42,6 +42,13 @@ def mx_scale_bytes(groups: int, rows: int, cols: int, ragged: bool = False) -> i
     return int(n)
 
 
+def _need_scales(groups, rows, cols, ragged=False):
+    """``mx_scale_bytes`` of a valid matrix, without a call into the library
+    (which checks the sizes again): include/moe.h has the layout."""
+    tiles = rows // 256 + min(rows, groups) if ragged else groups * ((rows + 255) // 256)
+    return max(tiles, 1) * 2048 * ((cols + 255) // 256)
+
+
 def _offsets(offsets, dev):
     """(pointer, groups) of ragged groups; offsets [groups + 1] int32."""
     if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.numel() < 2:
@@ -53,10 +60,13 @@ def _offsets(offsets, dev):
 def _check_mx(name, q, dev):
     if not isinstance(q, MXTensor):
         raise TypeError(f"{name} must be an MXTensor")
+    if not isinstance(q.data, torch.Tensor) or not isinstance(q.scales, torch.Tensor):
+        raise TypeError(f"{name}.data and {name}.scales must be tensors")
     if q.data.dim() not in (2, 3):
         raise ValueError(f"{name}.data must be [rows, cols / 2] or [groups, rows, cols / 2]")
-    need(f"{name}.data", q.data, _BYTE, None, dev)
-    need(f"{name}.scales", q.scales, _BYTE, None, dev)
+    for t in (q.data, q.scales):
+        if t.dtype is not _BYTE or t.device != dev or not t.is_contiguous():
+            raise ValueError(f"{name}.data and {name}.scales must be contiguous uint8 tensors on {dev}")
 
 
 def mx_quantize(x, offsets=None, *, stream=None) -> MXTensor:
@@ -73,10 +83,13 @@ def mx_quantize(x, offsets=None, *, stream=None) -> MXTensor:
     rows, cols = x.shape[-2], x.shape[-1]
     off, groups = _offsets(offsets, dev) if offsets is not None else (None, x.shape[0] if x.dim() == 3 else 1)
     with on(dev, stream) as s:
-        n = mx_scale_bytes(groups, rows, cols, offsets is not None)
+        if cols <= 0 or cols % 32 or groups <= 0:
+            mx_scale_bytes(groups, rows, cols, offsets is not None)  # raises, with the reason
+        n = _need_scales(groups, rows, cols, offsets is not None)
         data = x.new_empty((*x.shape[:-1], cols // 2), dtype=_BYTE)
-        scales = x.new_empty((n,), dtype=_BYTE)
-        check(lib.moe_mx_quantize(ptr(x), off, groups, rows, cols, dt, ptr(data), ptr(scales), n, s), lib)
+        scales = torch.empty_strided((n,), (1,), dtype=_BYTE, device=dev)
+        check(lib.moe_mx_quantize(x.data_ptr(), off, groups, rows, cols, dt, data.data_ptr(), scales.data_ptr(), n, s),
+              lib)
     return MXTensor(data, scales)
 
 
@@ -101,8 +114,8 @@ def mx_dequantize(q: MXTensor, dtype=torch.bfloat16, offsets=None, *, out=None, 
             out = q.data.new_empty(shape, dtype=dtype)
         else:
             need("out", out, dtype, shape, dev)
-        check(lib.moe_mx_dequantize(ptr(q.data), ptr(q.scales), q.scales.numel(), off, groups, rows, cols, dt,
-                                    ptr(out), s), lib)
+        check(lib.moe_mx_dequantize(q.data.data_ptr(), q.scales.data_ptr(), q.scales.numel(), off, groups, rows, cols,
+                                    dt, out.data_ptr(), s), lib)
     return out
 
 
@@ -135,9 +148,9 @@ def mx_matmul(a: MXTensor, b: MXTensor, offsets=None, *, out_dtype=torch.bfloat1
         raise ValueError(f"a has {2 * sa[-1]} columns and b {K}")
     lib = B.load_library()
     for name, q, g, rows, ragged in (("a", a, groups, M, off is not None), ("b", b, groups, N, False)):
-        n = mx_scale_bytes(g, rows, K, ragged)
-        if q.scales.numel() < n:
-            raise ValueError(f"{name}.scales holds {q.scales.numel()} bytes, {n} are needed")
+        if q.scales.numel() < _need_scales(g, rows, K, ragged):
+            raise ValueError(f"{name}.scales holds {q.scales.numel()} bytes, "
+                             f"{_need_scales(g, rows, K, ragged)} are needed")
     if status is None:
         status = device_status(dev)
     else:
@@ -148,8 +161,8 @@ def mx_matmul(a: MXTensor, b: MXTensor, offsets=None, *, out_dtype=torch.bfloat1
             out = a.data.new_empty(shape, dtype=out_dtype)
         else:
             need("out", out, out_dtype, shape, dev)
-        check(lib.moe_mx_matmul(ptr(a.data), ptr(a.scales), ptr(b.data), ptr(b.scales), off, groups, M, N, K, dt,
-                                ptr(out), ptr(status), s), lib)
+        check(lib.moe_mx_matmul(a.data.data_ptr(), a.scales.data_ptr(), b.data.data_ptr(), b.scales.data_ptr(), off,
+                                groups, M, N, K, dt, out.data_ptr(), status.data_ptr(), s), lib)
     return out
 
 
@@ -179,7 +192,7 @@ def _weights(w_gate, w_up, w_down, dev, d):
         if q.data.dim() != 3:
             raise ValueError(f"{name} must be [E, rows, cols]")
     E, I, _ = w_gate.data.shape
-    n_up, n_down = mx_scale_bytes(E, I, d), mx_scale_bytes(E, d, I)
+    n_up, n_down = _need_scales(E, I, d), _need_scales(E, d, I)
     for name, q, shape, n in (("w_gate", w_gate, (E, I, d), n_up), ("w_up", w_up, (E, I, d), n_up),
                               ("w_down", w_down, (E, d, I), n_down)):
         got = q.data.shape

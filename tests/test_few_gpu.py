@@ -241,3 +241,13 @@ def test_hidden_units_and_columns_that_end_inside_a_block():
         r = moe_forward_few(**p, k=1, renorm=True)
         assert (r.topk_idx == 0).all()
         check_out(p, r.topk_idx, r.topk_gate, r.out, dtype)
+
+
+def test_more_items_than_the_joins_may_lie_behind():
+    # 128 experts with a token each and 1024 blocks of columns: some 440 items for each of a block's two pipelines
+    p = layer(16, 16384, 128, 8, 8, 14, BF16)
+    p["b_router"] = torch.zeros_like(p["b_router"])
+    r = moe_forward_few(**p, k=8, renorm=True)
+    check_routing(p, 8, True, r.topk_idx, r.topk_gate)
+    check_out(p, r.topk_idx, r.topk_gate, r.out, BF16)
+    assert torch.equal(r.out, moe_forward_few(**p, k=8, renorm=True).out)
