@@ -179,6 +179,7 @@ moe_status mx_layer(const void* x, const void* w_router, const float* b_router, 
   err = launch_mx_dispatch(dtype, x, T, d, E, k, md, inv, rgate, xq, xq_sc, status, stream);
   if (err != cudaSuccess) return fail_cuda(err, "dispatch kernel");
   MxOut hid = {};
+  hid.form = kMxHidden;
   hid.h = h;
   hid.h_scales = h_sc;
   err = launch_mx_gateup(up, offsets, E, R, I, d, (int)mx_group_tiles(I), hid, status, stream);

@@ -113,6 +113,19 @@ __device__ __forceinline__ void transpose_units(uint32_t (&w)[4][4]) {
   }
 }
 
+// The larger of a and |b|; NaN if either is.
+__device__ __forceinline__ float max_abs_nan(float a, float b) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(fabsf(b)));
+  return m;
+}
+// 32 bytes at once, a whole sector.
+__device__ __forceinline__ void store_sector(void* p, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
 struct MxTile {
   int g, m, n, row0, cnt;  // group, 256-row tile, weight block, first row and rows of the group
 };
@@ -138,10 +151,10 @@ __device__ __forceinline__ MxTile mx_tile(int tile, int n_wb, const int* s_off, 
   return t;
 }
 
-// kGateUp: see above. Maps: codes of A and of the weights (boxes of 128 rows x
+// kForm: what is written (MxForm); the hidden rows: gate/up, see above. Maps: codes of A and of the weights (boxes of 128 rows x
 // 128 bytes), scales of A and of the weights (boxes of 1024 bytes). For the
 // product tmB1/tmSB1 repeat tmB0/tmSB0.
-template <bool kGateUp>
+template <int kForm>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
     mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA32,
                    const __grid_constant__ CUtensorMap tmSA,
@@ -149,6 +162,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
                    const __grid_constant__ CUtensorMap tmSB0, const __grid_constant__ CUtensorMap tmSB1,
                    const int32_t* __restrict__ offsets, int G, int M, int N, int K, int group_tiles,
                    const MxOut out, int32_t* status, uint64_t limit_ns) {
+  constexpr bool kGateUp = kForm == kMxHidden;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sA = smem;
@@ -372,6 +386,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
     const int rt = q * 32 + lane;  // row of this CTA's 128
     for (int tile = cid; tile < total; tile += ncl) {
       const MxTile t = mx_tile(tile, n_wb, s_off, s_mt, G);
+      const int first = t.m * 256 + (int)rank * 128 + q * 32;  // this warp's first row in its group
+      float gate = 0.f;  // asked for before the wait
+      if (kForm == kMxY16 && first + lane < t.cnt) gate = __ldg(out.gate + t.row0 + first + lane);
       if (!__all_sync(0xffffffffu, mbar_wait(tfull, acc_phase, s_abort, status, limit_ns))) break;
       acc_phase ^= 1u;
       tc_fence_after();
@@ -383,7 +400,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster_cta(tempty_leader);
-      const int first = t.m * 256 + (int)rank * 128 + q * 32;  // this warp's first row in its group
       if (first >= t.cnt) continue;  // none of them exists
       if (kGateUp) {
         const int unit0 = t.n * 128 + part * 32;
@@ -406,57 +422,57 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
           out.h_scales[mx_scale_at((size_t)(2 * (s_mt[t.g] + t.m) + (int)rank), mx_stages(N), rt, t.n * 4 + part)] =
               (uint8_t)sb;
         }
-      } else {
-        const int el = out.form == kMxF32 ? 4 : 2;
-        const int cols = 64 / el;  // of a pass
-        if (out.form == kMxY16) {
-          const float gs = first + lane < t.cnt ? out.gate[t.row0 + first + lane] : 0.f;
+      } else if (kForm == kMxY16) {
+        // 64 bytes of a row at a time, in two sectors
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
+        for (int c = 0; c < 2; ++c) {
+          float m = 0.f;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[c][i] = __float_as_uint(gs * __uint_as_float(v[c][i]));
+          for (int i = 0; i < 32; ++i) m = max_abs_nan(m, __uint_as_float(v[c][i]));
+          // the largest of the gated values: rounding does not change which it is
+          const uint32_t e = y16_exp(__float_as_uint(fabsf(gate) * m));
+          const float inv = y16_inv(e), f = gate * inv;
+          uint32_t w[16];
+          if (__all_sync(0xffffffffu, e != 0xffu && fabsf(f) <= 3.0e38f)) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] = y16_pack(__uint_as_float(v[c][2 * i]), __uint_as_float(v[c][2 * i + 1]), f);
+          } else {  // gate * inv out of range, or a block that is kept as bf16
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float x = gate * __uint_as_float(v[c][2 * i]), y = gate * __uint_as_float(v[c][2 * i + 1]);
+              w[i] = e == 0xffu ? pack_bf16x2(x, y) : y16_pack(x, y, inv);
+            }
+          }
+          const int col = t.n * 256 + part * 64 + c * 32;
+          const size_t row = (size_t)(t.row0 + first + lane);
+          if (first + lane < t.cnt && col < N) {
+            out.y_exp[y16_exp_at((size_t)M, col, row)] = (uint8_t)e;
+            uint8_t* dst = static_cast<uint8_t*>(out.out) + (row * N + col) * 2;
+            store_sector(dst, w);
+            store_sector(dst + 32, w + 8);
+          }
         }
-        // 64 bytes of every row, from column c0 of this warp's 64
-        auto pass = [&](int c0, uint32_t (&w)[4][4]) {
+      } else {
+        constexpr int el = kForm == kMxF32 ? 4 : 2, cols = 64 / el;  // columns of a pass
+        // 64 bytes of every row at a time
+#pragma unroll
+        for (int c = 0; c < el; ++c) {
+          uint32_t w[4][4];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            if (kForm == kMxF32)
+              w[i >> 2][i & 3] = v[c >> 1][(c & 1) * 16 + i];
+            else
+              w[i >> 2][i & 3] = pack_bf16x2(__uint_as_float(v[c & 1][2 * i]), __uint_as_float(v[c & 1][2 * i + 1]));
+          }
           transpose_units(w);
-          const int col = t.n * 256 + part * 64 + c0 + (lane & 3) * (cols / 4), r0 = lane & ~3;
+          const int col = t.n * 256 + part * 64 + c * cols + (lane & 3) * (cols / 4), r0 = lane & ~3;
           uint8_t* dst = static_cast<uint8_t*>(out.out) + ((size_t)(t.row0 + first + r0) * N + col) * el;
           if (col < N) {
 #pragma unroll
             for (int r = 0; r < 4; ++r)
               if (first + r0 + r < t.cnt)
                 *reinterpret_cast<uint4*>(dst + (size_t)r * N * el) = make_uint4(w[r][0], w[r][1], w[r][2], w[r][3]);
-          }
-        };
-        if (out.form == kMxF32) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t w[4][4];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) w[i >> 2][i & 3] = v[c >> 1][(c & 1) * 16 + i];
-            pass(c * 16, w);
-          }
-        } else {
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t w[4][4];
-            uint32_t e = 0xffu;
-            if (out.form == kMxY16) {
-              uint32_t m = 0;
-#pragma unroll
-              for (int i = 0; i < 32; ++i) m = max(m, v[c][i] & 0x7fffffffu);
-              e = y16_exp(m);
-              const int col = t.n * 256 + part * 64 + c * 32;
-              if (first + lane < t.cnt && col < N)
-                out.y_exp[y16_exp_at((size_t)M, col, (size_t)(t.row0 + first + lane))] = (uint8_t)e;
-            }
-            const float inv = y16_inv(e);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float x = __uint_as_float(v[c][2 * i]), y = __uint_as_float(v[c][2 * i + 1]);
-              w[i >> 2][i & 3] = e == 0xffu ? pack_bf16x2(x, y) : y16_pack(x, y, inv);
-            }
-            pass(c * 32, w);
           }
         }
       }
@@ -498,11 +514,12 @@ int max_pairs(const void* kern, std::atomic<int>* cache) {
   return n;
 }
 
-template <bool kGateUp>
+template <int kForm>
 cudaError_t launch(const MxMaps& m, const int32_t* offsets, int G, int M, int N, int K, int group_tiles,
                    const MxOut& out, int32_t* status, cudaStream_t stream) {
   static std::atomic<int> cache[64];
-  auto kern = mx_gemm_kernel<kGateUp>;
+  constexpr bool kGateUp = kForm == kMxHidden;
+  auto kern = mx_gemm_kernel<kForm>;
   const int pairs = max_pairs(reinterpret_cast<const void*>(kern), cache);
   if (pairs <= 0) return cudaErrorInvalidConfiguration;
   const long long n_wb = kGateUp ? (N + 127) / 128 : (N + 255) / 256;
@@ -518,12 +535,14 @@ cudaError_t launch(const MxMaps& m, const int32_t* offsets, int G, int M, int N,
 
 cudaError_t launch_mx_product(const MxMaps& m, const int32_t* offsets, int G, int M, int N, int K, int group_tiles,
                               const MxOut& out, int32_t* status, cudaStream_t stream) {
-  return launch<false>(m, offsets, G, M, N, K, group_tiles, out, status, stream);
+  if (out.form == kMxY16) return launch<kMxY16>(m, offsets, G, M, N, K, group_tiles, out, status, stream);
+  if (out.form == kMxF32) return launch<kMxF32>(m, offsets, G, M, N, K, group_tiles, out, status, stream);
+  return launch<kMxBf16>(m, offsets, G, M, N, K, group_tiles, out, status, stream);
 }
 
 cudaError_t launch_mx_gateup(const MxMaps& m, const int32_t* offsets, int G, int M, int N, int K, int group_tiles,
                              const MxOut& out, int32_t* status, cudaStream_t stream) {
-  return launch<true>(m, offsets, G, M, N, K, group_tiles, out, status, stream);
+  return launch<kMxHidden>(m, offsets, G, M, N, K, group_tiles, out, status, stream);
 }
 
 }  // namespace moe

@@ -31,7 +31,7 @@ struct MxMaps {
 // Where an MXFP4 product writes: out [M, N] in bf16, fp32 or, each row
 // multiplied by gate[row], as 16-bit numbers with their exponents in y_exp
 // (mx.cuh, y16); or for gate/up the MXFP4 hidden rows.
-enum MxForm { kMxBf16, kMxF32, kMxY16 };
+enum MxForm { kMxBf16, kMxF32, kMxY16, kMxHidden };
 struct MxOut {
   void* out;
   int form;
