@@ -89,17 +89,20 @@ __device__ __forceinline__ uint64_t scales_desc(uint32_t smem_addr) {
   return desc;
 }
 
-// Four lanes, each with four 16-byte units of its own row: lane l of the four
-// gets unit l of every one of their rows, so that a store of the warp writes
-// 64 consecutive bytes of eight rows.
-__device__ __forceinline__ void transpose_units(uint32_t (&w)[4][4]) {
+// kN lanes, each with kN 16-byte units of its own row: lane l of them gets
+// unit l of every one of their rows, so that a store of the warp writes 16 kN
+// consecutive bytes of a row. Whole lines (8) cost half as many shuffles again
+// and are better where a kernel's loads wait for its stores (the experts' down
+// product: 58 us against 63 for the fine-grained layer), half lines (4) where
+// HBM takes the results anyway (8192 x 14336 x 4096: 167 against 169).
+template <int kN>
+__device__ __forceinline__ void transpose_units(uint32_t (&w)[kN][4]) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    const int o = 1 << s;
+  for (int o = 1; o < kN; o <<= 1) {
     const bool up = lane & o;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
+    for (int u = 0; u < kN; ++u) {
       if (u & o) continue;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -119,13 +122,6 @@ __device__ __forceinline__ float max_abs_nan(float a, float b) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(fabsf(b)));
   return m;
 }
-// 32 bytes at once, a whole sector.
-__device__ __forceinline__ void store_sector(void* p, const uint32_t* v) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
-}
-
 struct MxTile {
   int g, m, n, row0, cnt;  // group, 256-row tile, weight block, first row and rows of the group
 };
@@ -422,55 +418,52 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
           out.h_scales[mx_scale_at((size_t)(2 * (s_mt[t.g] + t.m) + (int)rank), mx_stages(N), rt, t.n * 4 + part)] =
               (uint8_t)sb;
         }
-      } else if (kForm == kMxY16) {
-        // 64 bytes of a row at a time, in two sectors
+      } else {
+        // kN units of every row at a time
+        constexpr int kN = kForm == kMxY16 ? 8 : 4;
+        constexpr int el = kForm == kMxF32 ? 4 : 2, cols = 16 * kN / el;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float m = 0.f;
+        for (int p = 0; p < 64 / cols; ++p) {
+          uint32_t w[kN][4];
+          if (kForm == kMxF32) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) m = max_abs_nan(m, __uint_as_float(v[c][i]));
-          // the largest of the gated values: rounding does not change which it is
-          const uint32_t e = y16_exp(__float_as_uint(fabsf(gate) * m));
-          const float inv = y16_inv(e), f = gate * inv;
-          uint32_t w[16];
-          if (__all_sync(0xffffffffu, e != 0xffu && fabsf(f) <= 3.0e38f)) {
+            for (int i = 0; i < cols; ++i) w[i >> 2][i & 3] = v[p >> 1][(p & 1) * 16 + i];
+          } else if (kForm == kMxBf16) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) w[i] = y16_pack(__uint_as_float(v[c][2 * i]), __uint_as_float(v[c][2 * i + 1]), f);
-          } else {  // gate * inv out of range, or a block that is kept as bf16
+            for (int i = 0; i < 16; ++i)
+              w[i >> 2][i & 3] = pack_bf16x2(__uint_as_float(v[p & 1][2 * i]), __uint_as_float(v[p & 1][2 * i + 1]));
+          } else {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float x = gate * __uint_as_float(v[c][2 * i]), y = gate * __uint_as_float(v[c][2 * i + 1]);
-              w[i] = e == 0xffu ? pack_bf16x2(x, y) : y16_pack(x, y, inv);
+            for (int c = 0; c < 2; ++c) {
+              float m = 0.f;
+#pragma unroll
+              for (int i = 0; i < 32; ++i) m = max_abs_nan(m, __uint_as_float(v[c][i]));
+              // the largest of the gated values: rounding does not change which it is
+              const uint32_t e = y16_exp(__float_as_uint(fabsf(gate) * m));
+              const float inv = y16_inv(e), f = gate * inv;
+              if (__all_sync(0xffffffffu, e != 0xffu && fabsf(f) <= 3.0e38f)) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                  w[(4 * c + (i >> 2)) % kN][i & 3] =
+                      y16_pack(__uint_as_float(v[c][2 * i]), __uint_as_float(v[c][2 * i + 1]), f);
+              } else {  // gate * inv out of range, or a block that is kept as bf16
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  const float x = gate * __uint_as_float(v[c][2 * i]), y = gate * __uint_as_float(v[c][2 * i + 1]);
+                  w[(4 * c + (i >> 2)) % kN][i & 3] = e == 0xffu ? pack_bf16x2(x, y) : y16_pack(x, y, inv);
+                }
+              }
+              const int col = t.n * 256 + part * 64 + c * 32;
+              if (first + lane < t.cnt && col < N)
+                out.y_exp[y16_exp_at((size_t)M, col, (size_t)(t.row0 + first + lane))] = (uint8_t)e;
             }
           }
-          const int col = t.n * 256 + part * 64 + c * 32;
-          const size_t row = (size_t)(t.row0 + first + lane);
-          if (first + lane < t.cnt && col < N) {
-            out.y_exp[y16_exp_at((size_t)M, col, row)] = (uint8_t)e;
-            uint8_t* dst = static_cast<uint8_t*>(out.out) + (row * N + col) * 2;
-            store_sector(dst, w);
-            store_sector(dst + 32, w + 8);
-          }
-        }
-      } else {
-        constexpr int el = kForm == kMxF32 ? 4 : 2, cols = 64 / el;  // columns of a pass
-        // 64 bytes of every row at a time
-#pragma unroll
-        for (int c = 0; c < el; ++c) {
-          uint32_t w[4][4];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            if (kForm == kMxF32)
-              w[i >> 2][i & 3] = v[c >> 1][(c & 1) * 16 + i];
-            else
-              w[i >> 2][i & 3] = pack_bf16x2(__uint_as_float(v[c & 1][2 * i]), __uint_as_float(v[c & 1][2 * i + 1]));
-          }
           transpose_units(w);
-          const int col = t.n * 256 + part * 64 + c * cols + (lane & 3) * (cols / 4), r0 = lane & ~3;
+          const int col = t.n * 256 + part * 64 + p * cols + (lane & (kN - 1)) * (16 / el), r0 = lane & ~(kN - 1);
           uint8_t* dst = static_cast<uint8_t*>(out.out) + ((size_t)(t.row0 + first + r0) * N + col) * el;
           if (col < N) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
+            for (int r = 0; r < kN; ++r)
               if (first + r0 + r < t.cnt)
                 *reinterpret_cast<uint4*>(dst + (size_t)r * N * el) = make_uint4(w[r][0], w[r][1], w[r][2], w[r][3]);
           }
