@@ -2,6 +2,10 @@
 // of given choices (the count of every expert's rows and each assignment's
 // rank), the quantisation of every token's row on its way into
 // expert-contiguous order, and the sum of each token's expert rows.
+//
+// All of it moves memory. Measured with cold caches, 4096 tokens of the
+// fine-grained layer (d 2048, 64 experts, k 6): count 5 us, dispatch 15 us (17 MB
+// read, 27 MB written), sum 23 us (102 MB read, 17 MB written: 5.2 TB/s).
 #include "mx.cuh"
 #include "mx_internal.h"
 

@@ -251,3 +251,25 @@ def test_more_items_than_the_joins_may_lie_behind():
     check_routing(p, 8, True, r.topk_idx, r.topk_gate)
     check_out(p, r.topk_idx, r.topk_gate, r.out, BF16)
     assert torch.equal(r.out, moe_forward_few(**p, k=8, renorm=True).out)
+
+
+def test_a_prompt_through_mxfp4_experts_and_then_single_tokens():
+    """As a server uses them: the experts are quantised once, the prompt and a batch of next tokens go through
+    moe_forward_mx, and one user's next tokens through moe_forward_few on the weights' values."""
+    from sparse_mixture_experts_renorm_b200 import moe_forward_mx, mx_dequantize, mx_experts, mx_quantize
+
+    p = layer(90, 256, 8, 2, 320, 15, BF16)
+    mx = [mx_quantize(p[n]) for n in ("w_gate", "w_up", "w_down")]
+    q = dict(p, **{n: mx_dequantize(t) for n, t in zip(("w_gate", "w_up", "w_down"), mx)})
+    prompt = moe_forward_mx(p["x"], p["w_router"], p["b_router"], *mx, k=2, renorm=True)
+    assert int(prompt.status) == 0
+    x = prompt.out[-3:].contiguous()
+    for step in range(3):
+        x = x / x.float().square().mean(1, keepdim=True).sqrt().to(BF16)
+        few = moe_forward_few(**dict(q, x=x), k=2, renorm=True)
+        batch = moe_forward_mx(x, p["w_router"], p["b_router"], *mx, k=2, renorm=True)
+        assert torch.equal(few.topk_idx, batch.topk_idx)
+        check_out(dict(q, x=x), few.topk_idx, few.topk_gate, few.out, BF16)
+        assert torch.equal(batch.out, mx_experts(x, batch.topk_idx, batch.topk_gate, *mx).out)
+        x = few.out
+    assert int(device_status("cuda").item()) == 0
