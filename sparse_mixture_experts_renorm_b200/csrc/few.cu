@@ -70,6 +70,7 @@ struct Plan {
   int expert[kMaxRows];             // ascending
   int base[kMaxRows + 1];           // first row of each
   int tj[kMaxRows];                 // t * k + j of a row
+  int tok[kMaxRows];                // and t
   float gate[kMaxRows];
   uint32_t mask[kMaxExperts];       // tokens of an expert
   int slot[kMaxExperts];
@@ -79,7 +80,8 @@ struct Plan {
 struct Group {
   uint64_t full[kMaxStages];   // the producers' bytes
   uint64_t empty[kMaxStages];  // the math warps
-  int item[kMaxStages];        // few_down: the item that a stage begins, or -1: there are no more
+  int4 item[kMaxStages];       // few_down: a stage's item: active expert + 256 x part (-1: there are no more),
+                               // block, chunks from and to
   int blk[kJoinQueue];         // few_down: block of output columns of each finished item
   volatile int finished;       // items whose parts are written; negative: ~items, and there are no more
   volatile int joined;         // items that have been counted
@@ -270,6 +272,7 @@ __device__ void make_plan(const FewArgs& a, Plan& p, const int* idx, const float
     const int e = idx[i], t = i / k;
     const int row = p.base[p.slot[e]] + __popc(p.mask[e] & ((1u << t) - 1u));
     p.tj[row] = i;
+    p.tok[row] = t;
     p.gate[row] = gate[i];
   }
   __syncthreads();
@@ -288,6 +291,7 @@ __device__ void logits_part(const X* __restrict__ x, const X* __restrict__ wr, i
   for (int e0 = 0; e0 < E; e0 += kPassE) {
     const int ne = min(kPassE, E - e0);
     float* mine = scratch + warp * kFewTokens * kPassLd;
+    int parts = kWarps;  // partial sums of a logit in this CTA
     if constexpr (sizeof(X) == 2) {
       float acc[kPassE / 16][2][4];
 #pragma unroll
@@ -328,34 +332,41 @@ __device__ void logits_part(const X* __restrict__ x, const X* __restrict__ wr, i
             if (m * 16 < ne) mine[t * kPassLd + e] = acc[m][n][i];
           }
     } else {
-      for (int e = 0; e < ne; e += 4)
-        for (int t = 0; t < T; t += 4) {
-          float v[16];
+      // blocks of 4 experts x 4 tokens over the warps; where there are fewer
+      // than warps, the columns too
+      const int pe = (ne + 3) / 4, pairs = pe * ((T + 3) / 4);
+      parts = max(1, kWarps / pairs);
+      const int slice = parts > 1 ? warp / pairs : 0;
+      mine = scratch + slice * kFewTokens * kPassLd;
+      for (int p = parts > 1 ? (slice < parts ? warp % pairs : pairs) : warp; p < pairs; p += parts > 1 ? pairs : kWarps) {
+        const int t = p / pe * 4, e = p % pe * 4;
+        float v[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] = 0.f;
-          for (int col = c0 + warp * 128 + lane * 4; col < c1; col += kWarps * 128) {
-            float4 a[4], b[4];
+        for (int i = 0; i < 16; ++i) v[i] = 0.f;
+#pragma unroll 2
+        for (int col = c0 + slice * 128 + lane * 4; col < c1; col += parts * 128) {
+          float4 a[4], b[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              a[i] = __ldg(reinterpret_cast<const float4*>(wr + (size_t)(e0 + min(e + i, ne - 1)) * d + col));
-              b[i] = __ldg(reinterpret_cast<const float4*>(x + (size_t)min(t + i, T - 1) * d + col));
-            }
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float4 &p = a[i >> 2], &q = b[i & 3];
-              v[i] = fmaf(p.w, q.w, fmaf(p.z, q.z, fmaf(p.y, q.y, fmaf(p.x, q.x, v[i]))));
-            }
+          for (int i = 0; i < 4; ++i) {
+            a[i] = __ldg(reinterpret_cast<const float4*>(wr + (size_t)(e0 + min(e + i, ne - 1)) * d + col));
+            b[i] = __ldg(reinterpret_cast<const float4*>(x + (size_t)min(t + i, T - 1) * d + col));
           }
-          const float s = reduce_many(v);
-          if ((lane & 1) == 0) mine[(t + ((lane >> 1) & 3)) * kPassLd + e + (lane >> 3)] = s;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float4 &q = a[i >> 2], &r = b[i & 3];
+            v[i] = fmaf(q.w, r.w, fmaf(q.z, r.z, fmaf(q.y, r.y, fmaf(q.x, r.x, v[i]))));
+          }
         }
+        const float s = reduce_many(v);
+        if ((lane & 1) == 0) mine[(t + ((lane >> 1) & 3)) * kPassLd + e + (lane >> 3)] = s;
+      }
     }
     __syncthreads();
     for (int i = threadIdx.x; i < ne * T; i += blockDim.x) {
       const int t = i / ne, e = i - t * ne;
       float s = rank == 0 ? bias[e0 + e] : 0.f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) s += scratch[(w * kFewTokens + t) * kPassLd + e];
+#pragma unroll 4
+      for (int w = 0; w < parts; ++w) s += scratch[(w * kFewTokens + t) * kPassLd + e];
       float* dst = part + ((size_t)rank * T + t) * E + e0 + e;
       for (int c = 0; c < kCluster; ++c) store_cluster(map_to_cta(dst, c), s);
     }
@@ -502,6 +513,21 @@ struct Work {
   }
 };
 
+// few_up's items of one group, one after the other without divisions: `step`
+// items further each time.
+struct Walk {
+  int s, blk, step_s, step_blk, n_blk;
+  __device__ __forceinline__ Walk(int first, int step, int blocks) : n_blk(blocks) {
+    s = first / blocks, blk = first - s * blocks;
+    step_s = step / blocks, step_blk = step - step_s * blocks;
+  }
+  __device__ __forceinline__ void next() {
+    s += step_s;
+    blk += step_blk;
+    if (blk >= n_blk) blk -= n_blk, ++s;
+  }
+};
+
 // Ring position.
 struct Pos {
   int stage = 0;
@@ -576,10 +602,9 @@ __device__ bool produce_up_weights(const FewMaps& maps, const FewArgs& a, Ctrl& 
                                    int step, Pos& pos, int& issued) {
   const Work<X, true> work(a, c.plan.n_act, 1);
   const int row_bytes = a.d * (int)sizeof(X);
-  for (int i = first; i < work.total; i += step) {
-    const Item w = work.item(i);
+  for (Walk w(first, step, work.n_blk); w.s < c.plan.n_act; w.next()) {
     const int row = c.plan.expert[w.s] * a.I + w.blk * 8;
-    for (int ch = w.c0; ch < w.c1; ++ch) {
+    for (int ch = 0; ch < work.chunks; ++ch) {
       if (!mbar_wait(&g.empty[pos.stage], pos.phase ^ 1u, &c.abort, a.status, a.limit_ns)) return false;
       mbar_arrive_expect_tx(&g.full[pos.stage], weight_bytes<X, true>(ch, row_bytes));
       load_weights<X, true>(maps, ring.base + (size_t)pos.stage * ring.slot, &g.full[pos.stage], ch, row, row_bytes);
@@ -597,16 +622,16 @@ __device__ bool produce_up_tokens(const FewArgs& a, Ctrl& c, Group& g, const Rin
   const int lane = threadIdx.x & 31;
   const Work<X, true> work(a, c.plan.n_act, 1);
   const int row_bytes = a.d * (int)sizeof(X);
-  for (int i = first; i < work.total; i += step) {
-    const Item w = work.item(i, c.plan);
+  for (Walk w(first, step, work.n_blk); w.s < c.plan.n_act; w.next()) {
+    const int n0 = c.plan.base[w.s], n = c.plan.base[w.s + 1] - n0;
     const uint8_t* src = nullptr;
-    if (lane < w.n) src = static_cast<const uint8_t*>(a.x) + (size_t)(c.plan.tj[w.first + lane] / a.k) * row_bytes;
-    for (int ch = w.c0; ch < w.c1; ++ch) {
+    if (lane < n) src = static_cast<const uint8_t*>(a.x) + (size_t)c.plan.tok[n0 + lane] * row_bytes;
+    for (int ch = 0; ch < work.chunks; ++ch) {
       const uint32_t bytes = (uint32_t)min(kChunk, row_bytes - ch * kChunk);
       bool free = true;
       if (lane == 0) {
         free = mbar_wait(&g.empty[pos.stage], pos.phase ^ 1u, &c.abort, a.status, a.limit_ns);
-        if (free) mbar_arrive_expect_tx(&g.full[pos.stage], w.n * bytes);
+        if (free) mbar_arrive_expect_tx(&g.full[pos.stage], n * bytes);
       }
       if (!__shfl_sync(0xffffffffu, (int)free, 0)) return false;
       if (src)
@@ -637,7 +662,7 @@ __device__ bool produce_down(const FewMaps& maps, const FewArgs& a, Ctrl& c, Gro
     if (more) w = work.item(i, c.plan);
     for (int ch = w.c0; ch < (more ? w.c1 : w.c0 + 1); ++ch) {
       if (!mbar_wait(&g.empty[pos.stage], pos.phase ^ 1u, &c.abort, a.status, a.limit_ns)) return false;
-      g.item[pos.stage] = more ? i : -1;
+      g.item[pos.stage] = make_int4(more ? w.s | w.part << 8 : -1, w.blk, w.c0, w.c1);
       const uint32_t bytes = (uint32_t)(w.n * Traits<X>::kHid * kTokPitch);
       if (more) {
         mbar_arrive_expect_tx(&g.full[pos.stage], weight_bytes<X, false>(ch, row_bytes) + bytes);
@@ -819,8 +844,10 @@ __device__ void consume_up(const FewArgs& a, Ctrl& c, Group& g, const Ring& ring
   const int tid = threadIdx.x - (group * kGroupWarps + 2) * 32;
   Pos pos;
   int buf = 0;
-  for (int i = first; i < work.total; i += step) {
-    const Item w = work.item(i, c.plan);
+  for (Walk at(first, step, work.n_blk); at.s < c.plan.n_act; at.next()) {
+    Item w;
+    w.s = at.s, w.blk = at.blk, w.part = 0, w.c0 = 0, w.c1 = work.chunks;
+    w.first = c.plan.base[w.s], w.n = c.plan.base[w.s + 1] - w.first;
     float* red = red2 + buf * red_floats<X>();
     buf ^= 1;
     const bool ok =
@@ -915,7 +942,6 @@ __device__ void join(const FewArgs& a, Ctrl& c, Group& g, const Work<X, false>& 
 // few_down's products.
 template <typename X>
 __device__ void consume_down(const FewArgs& a, Ctrl& c, Group& g, const Ring& ring, float* red2, int group) {
-  const Work<X, false> work(a, c.plan.n_act, c.plan.down_split);
   const int tid = threadIdx.x - (group * kGroupWarps + 2) * 32;
   const int R = a.T * a.k;
   Pos pos;
@@ -923,8 +949,11 @@ __device__ void consume_down(const FewArgs& a, Ctrl& c, Group& g, const Ring& ri
   for (int n_item = 0;; ++n_item) {
     // the stage says which item begins
     bool ok = __all_sync(0xffffffffu, mbar_wait(&g.full[pos.stage], pos.phase, &c.abort, a.status, a.limit_ns));
-    const int i = ok ? g.item[pos.stage] : -1;
-    const Item w = work.item(max(i, 0), c.plan);
+    const int4 at = ok ? g.item[pos.stage] : make_int4(-1, 0, 0, 0);
+    const int i = at.x;
+    Item w;
+    w.s = max(at.x, 0) & 0xff, w.part = max(at.x, 0) >> 8, w.blk = at.y, w.c0 = at.z, w.c1 = at.w;
+    w.first = c.plan.base[w.s], w.n = c.plan.base[w.s + 1] - w.first;
     float* red = red2 + buf * red_floats<X>();
     buf ^= 1;
     if (i >= 0)
