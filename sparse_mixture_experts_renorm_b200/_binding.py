@@ -176,6 +176,9 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.moe_few_workspace_size.restype = SZ
     lib.moe_forward_few.argtypes = lib.moe_forward.argtypes
     lib.moe_forward_few.restype = I32
+    for name in ("forward_few", "mx_quantize", "mx_dequantize", "mx_matmul", "mx_experts"):  # csrc/bind.cu
+        f = getattr(lib, "moe_bind_" + name)
+        f.argtypes, f.restype = [ctypes.c_char_p], I32
     lib.moe_last_error_detail.argtypes = [ctypes.c_char_p, SZ]
     lib.moe_last_error_detail.restype = SZ
     if path is None:

@@ -3,6 +3,7 @@ stream and device of a call, and the status word of calls without one."""
 from __future__ import annotations
 
 import contextlib
+import struct
 
 import torch
 
@@ -21,6 +22,11 @@ def dtype_code(t: torch.dtype) -> int:
     if t == torch.float32:
         return B.MOE_F32
     raise TypeError(f"unsupported dtype {t}: bfloat16 or float32 is needed")
+
+
+def record(n):
+    """Packs n numbers (pointers, sizes, flags) for a moe_bind_* function."""
+    return struct.Struct(f"{n}q").pack
 
 
 def ptr(t):

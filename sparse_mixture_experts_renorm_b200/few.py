@@ -7,7 +7,9 @@ from dataclasses import dataclass
 import torch
 
 from . import _binding as B
-from ._call import check, cuda, device_status, dtype_code, need, on, ptr
+from ._call import check, cuda, device_status, dtype_code, need, on, record
+
+_args = record(22)
 
 
 @dataclass(slots=True)
@@ -77,8 +79,9 @@ def moe_forward_few(x, w_router, b_router, w_gate, w_up, w_down, k: int, renorm:
             topk_gate = torch.empty_strided((T, k), (k, 1), dtype=torch.float32, device=dev)
         else:
             need("topk_gate", topk_gate, torch.float32, (T, k), dev)
-        check(lib.moe_forward_few(x.data_ptr(), w_router.data_ptr(), ptr(b_router), w_gate.data_ptr(),
-                                  w_up.data_ptr(), w_down.data_ptr(), T, d, E, k, I, 1 if renorm else 0, code,
-                                  out.data_ptr(), topk_idx.data_ptr(), topk_gate.data_ptr(), ptr(counts), ptr(aux),
-                                  workspace.data_ptr(), workspace.numel(), status.data_ptr(), s), lib)
+        check(lib.moe_bind_forward_few(_args(
+            x.data_ptr(), w_router.data_ptr(), 0 if b_router is None else b_router.data_ptr(), w_gate.data_ptr(),
+            w_up.data_ptr(), w_down.data_ptr(), T, d, E, k, I, 1 if renorm else 0, code, out.data_ptr(),
+            topk_idx.data_ptr(), topk_gate.data_ptr(), 0 if counts is None else counts.data_ptr(),
+            0 if aux is None else aux.data_ptr(), workspace.data_ptr(), workspace.numel(), status.data_ptr(), s)), lib)
     return FewOutputs(out, topk_idx, topk_gate, status, counts, aux)

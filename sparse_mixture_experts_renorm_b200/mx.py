@@ -9,9 +9,10 @@ from dataclasses import dataclass
 import torch
 
 from . import _binding as B
-from ._call import check, cuda, device_status, dtype_code, need, on, ptr
+from ._call import check, cuda, device_status, dtype_code, need, on, ptr, record
 
 _BYTE = torch.uint8
+_args10, _args13, _args21 = record(10), record(13), record(21)
 
 
 @dataclass(slots=True)
@@ -81,15 +82,15 @@ def mx_quantize(x, offsets=None, *, stream=None) -> MXTensor:
     need("x", x, x.dtype, None, dev)
     lib = B.load_library()
     rows, cols = x.shape[-2], x.shape[-1]
-    off, groups = _offsets(offsets, dev) if offsets is not None else (None, x.shape[0] if x.dim() == 3 else 1)
+    off, groups = _offsets(offsets, dev) if offsets is not None else (0, x.shape[0] if x.dim() == 3 else 1)
     with on(dev, stream) as s:
         if cols <= 0 or cols % 32 or groups <= 0:
             mx_scale_bytes(groups, rows, cols, offsets is not None)  # raises, with the reason
         n = _need_scales(groups, rows, cols, offsets is not None)
         data = x.new_empty((*x.shape[:-1], cols // 2), dtype=_BYTE)
         scales = torch.empty_strided((n,), (1,), dtype=_BYTE, device=dev)
-        check(lib.moe_mx_quantize(x.data_ptr(), off, groups, rows, cols, dt, data.data_ptr(), scales.data_ptr(), n, s),
-              lib)
+        check(lib.moe_bind_mx_quantize(_args10(x.data_ptr(), off, groups, rows, cols, dt, data.data_ptr(),
+                                               scales.data_ptr(), n, s)), lib)
     return MXTensor(data, scales)
 
 
@@ -108,14 +109,14 @@ def mx_dequantize(q: MXTensor, dtype=torch.bfloat16, offsets=None, *, out=None, 
     lib = B.load_library()
     rows, cols = shape[-2], 2 * shape[-1]
     shape = (*shape[:-1], cols)
-    off, groups = _offsets(offsets, dev) if offsets is not None else (None, shape[0] if len(shape) == 3 else 1)
+    off, groups = _offsets(offsets, dev) if offsets is not None else (0, shape[0] if len(shape) == 3 else 1)
     with on(dev, stream) as s:
         if out is None:
             out = q.data.new_empty(shape, dtype=dtype)
         else:
             need("out", out, dtype, shape, dev)
-        check(lib.moe_mx_dequantize(q.data.data_ptr(), q.scales.data_ptr(), q.scales.numel(), off, groups, rows, cols,
-                                    dt, out.data_ptr(), s), lib)
+        check(lib.moe_bind_mx_dequantize(_args10(q.data.data_ptr(), q.scales.data_ptr(), q.scales.numel(), off, groups,
+                                                 rows, cols, dt, out.data_ptr(), s)), lib)
     return out
 
 
@@ -137,7 +138,7 @@ def mx_matmul(a: MXTensor, b: MXTensor, offsets=None, *, out_dtype=torch.bfloat1
     groups = sb[0] if len(sb) == 3 else 1
     N, K = sb[-2], 2 * sb[-1]
     M = sa[-2]
-    off = None
+    off = 0
     if offsets is not None:
         off, n = _offsets(offsets, dev)
         if len(sa) != 2 or n != groups:
@@ -147,7 +148,7 @@ def mx_matmul(a: MXTensor, b: MXTensor, offsets=None, *, out_dtype=torch.bfloat1
     if 2 * sa[-1] != K:
         raise ValueError(f"a has {2 * sa[-1]} columns and b {K}")
     lib = B.load_library()
-    for name, q, g, rows, ragged in (("a", a, groups, M, off is not None), ("b", b, groups, N, False)):
+    for name, q, g, rows, ragged in (("a", a, groups, M, offsets is not None), ("b", b, groups, N, False)):
         if q.scales.numel() < _need_scales(g, rows, K, ragged):
             raise ValueError(f"{name}.scales holds {q.scales.numel()} bytes, "
                              f"{_need_scales(g, rows, K, ragged)} are needed")
@@ -161,8 +162,9 @@ def mx_matmul(a: MXTensor, b: MXTensor, offsets=None, *, out_dtype=torch.bfloat1
             out = a.data.new_empty(shape, dtype=out_dtype)
         else:
             need("out", out, out_dtype, shape, dev)
-        check(lib.moe_mx_matmul(a.data.data_ptr(), a.scales.data_ptr(), b.data.data_ptr(), b.scales.data_ptr(), off,
-                                groups, M, N, K, dt, out.data_ptr(), status.data_ptr(), s), lib)
+        check(lib.moe_bind_mx_matmul(_args13(a.data.data_ptr(), a.scales.data_ptr(), b.data.data_ptr(),
+                                             b.scales.data_ptr(), off, groups, M, N, K, dt, out.data_ptr(),
+                                             status.data_ptr(), s)), lib)
     return out
 
 
@@ -200,10 +202,8 @@ def _weights(w_gate, w_up, w_down, dev, d):
             raise ValueError(f"{name} must have the shape {shape} (got {tuple(q.shape)})")
         if q.scales.numel() < n:
             raise ValueError(f"{name}.scales holds {q.scales.numel()} bytes, {n} are needed")
-    w = B.moe_mx_weights(ctypes.sizeof(B.moe_mx_weights), w_gate.data.data_ptr(), w_gate.scales.data_ptr(),
-                         w_up.data.data_ptr(), w_up.scales.data_ptr(), w_down.data.data_ptr(),
-                         w_down.scales.data_ptr())
-    return w, E, I
+    return (w_gate.data.data_ptr(), w_gate.scales.data_ptr(), w_up.data.data_ptr(), w_up.scales.data_ptr(),
+            w_down.data.data_ptr(), w_down.scales.data_ptr()), E, I
 
 
 def _buffers(x, T, d, E, k, I, out, counts, workspace, status):
@@ -257,8 +257,10 @@ def mx_experts(x, topk_idx, topk_gate, w_gate: MXTensor, w_up: MXTensor, w_down:
     lib = B.load_library()
     with on(dev, stream) as s:
         out, counts, workspace = _buffers(x, T, d, E, k, I, out, counts, workspace, status)
-        check(lib.moe_mx_experts(ptr(x), ptr(topk_idx), ptr(topk_gate), ctypes.byref(w), T, d, E, k, I, dt, ptr(out),
-                                 ptr(counts), ptr(workspace), workspace.numel(), ptr(status), s), lib)
+        check(lib.moe_bind_mx_experts(_args21(
+            x.data_ptr(), topk_idx.data_ptr(), topk_gate.data_ptr(), *w, T, d, E, k, I, dt, out.data_ptr(),
+            counts.data_ptr(), workspace.data_ptr(), workspace.numel(), 0 if status is None else status.data_ptr(),
+            s)), lib)
         status = _status_of(status, workspace)
     return MXOutputs(out, counts, status, workspace)
 
@@ -287,7 +289,8 @@ def moe_forward_mx(x, w_router, b_router, w_gate: MXTensor, w_up: MXTensor, w_do
         need("topk_idx", topk_idx, torch.int32, (T, k), dev)
         need("topk_gate", topk_gate, torch.float32, (T, k), dev)
         need("aux", aux, torch.float32, (1,), dev)
-        check(lib.moe_mx_forward(ptr(x), ptr(w_router), ptr(b_router), ctypes.byref(w), T, d, E, k, I,
+        weights = B.moe_mx_weights(ctypes.sizeof(B.moe_mx_weights), *w)
+        check(lib.moe_mx_forward(ptr(x), ptr(w_router), ptr(b_router), ctypes.byref(weights), T, d, E, k, I,
                                  int(bool(renorm)), dt, ptr(out), ptr(topk_idx), ptr(topk_gate), ptr(counts),
                                  ptr(aux), ptr(workspace), workspace.numel(), ptr(status), s), lib)
         status = _status_of(status, workspace)
