@@ -26,10 +26,10 @@
 // finish adds them up, in a fixed order whatever the order of arrival.
 //
 // Measured (bf16, us and bytes that it cannot do without over the time): 16
-// tokens of the Mixtral-shaped layer (d 4096, I 14336, 8 experts, k 2) 436 us,
-// 6.4 TB/s; 5 tokens of the fine-grained one (d 2048, I 1408, 64 experts, k 6)
-// 80 us, 5.4 TB/s; one token of the small one (d 1024, I 2816, 8 experts, k 2)
-// 22 us, 1.6 TB/s. What is left there: some 8 us from the launch to the first
+// tokens of the Mixtral-shaped layer (d 4096, I 14336, 8 experts, k 2) 422 us,
+// 6.6 TB/s; 5 tokens of the fine-grained one (d 2048, I 1408, 64 experts, k 6)
+// 77 us, 5.6 TB/s; one token of the small one (d 1024, I 2816, 8 experts, k 2)
+// 21 us, 1.6 TB/s. What is left there: some 8 us from the launch to the first
 // weight (3.6 us of logits, 2.5 us of choosing and 1.3 us of grouping for 64
 // experts; half of that for 8), 4 us between the kernels, and the last items'
 // and joins' tail.
