@@ -446,7 +446,8 @@ moe_status moe_mx_matmul(const void* a, const void* a_scales, const void* b, con
  * be NULL.
  * moe_mx_forward runs the router before them; arguments and outputs as for
  * moe_forward (x and w_router in `dtype`, with the limits of its router).
- * workspace: moe_mx_workspace_size() bytes, 256-byte aligned, any contents.
+ * workspace: moe_mx_workspace_size() bytes, 256-byte aligned, any contents;
+ * calls that overlap on the GPU need one each.
  * Results are bit-identical from run to run.
  */
 typedef struct moe_mx_weights {

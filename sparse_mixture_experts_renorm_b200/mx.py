@@ -244,8 +244,9 @@ def mx_experts(x, topk_idx, topk_gate, w_gate: MXTensor, w_up: MXTensor, w_down:
     """The layer's experts in MXFP4 for given choices: ``x`` [T, d] (bf16 or
     fp32), ``topk_idx`` [T, k] int32, ``topk_gate`` [T, k] fp32, weights
     [E, I, d], [E, I, d] and [E, d, I]. out[t] = sum_j gate[t, j] y of expert
-    idx[t, j], bf16. Without ``status`` the call's word is the workspace's
-    first four bytes (cleared by the call)."""
+    idx[t, j], bf16. ``workspace``: uint8, ``mx_workspace_size`` bytes, one for
+    each call that may run at the same time. Without ``status`` the call's word
+    is the workspace's first four bytes (cleared by the call)."""
     dev, dt = _rows(x)
     T, d = x.shape
     w, E, I = _weights(w_gate, w_up, w_down, dev, d)

@@ -273,3 +273,20 @@ def test_a_prompt_through_mxfp4_experts_and_then_single_tokens():
         assert torch.equal(batch.out, mx_experts(x, batch.topk_idx, batch.topk_gate, *mx).out)
         x = few.out
     assert int(device_status("cuda").item()) == 0
+
+
+@pytest.mark.parametrize("change,error", [
+    (dict(x=lambda p: p["x"].t().contiguous().t()), ValueError), (dict(x=lambda p: p["x"].float()), ValueError),
+    (dict(x=lambda p: p["x"].half()), TypeError), (dict(x=lambda p: p["x"].cpu()), ValueError),
+    (dict(w_down=lambda p: p["w_down"].transpose(1, 2)), ValueError), (dict(w_up=lambda p: p["w_up"][:, ::2]), ValueError),
+    (dict(w_router=lambda p: p["w_router"][:-1]), ValueError), (dict(b_router=lambda p: p["b_router"].double()), ValueError),
+    (dict(out=lambda p: torch.empty((4, 128), device="cuda")), ValueError),
+    (dict(workspace=lambda p: torch.empty((64,), dtype=torch.uint8, device="cuda")), B.MoEError),
+    (dict(status=lambda p: torch.zeros((2,), dtype=torch.int32, device="cuda")), ValueError),
+    (dict(x=lambda p: p["x"].repeat(5, 1)), B.MoEError), (dict(k=lambda p: 9), B.MoEError), (dict(k=lambda p: 0), B.MoEError)])
+def test_refusals(change, error):
+    p = layer(4, 128, 8, 2, 64, 16, BF16)
+    args = dict(p, k=2, renorm=True)
+    args.update({n: f(p) for n, f in change.items()})
+    with pytest.raises(error):
+        moe_forward_few(**args)

@@ -339,3 +339,33 @@ def test_experts_on_a_stream_in_a_graph_and_after_other_work_in_the_workspace():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, mx_experts(x * scale, idx, gate, *w).out)
+
+
+def test_refusals_of_the_wrappers():
+    x, idx, gate, w = layer(20, 64, 4, 2, 64, 18)
+    q = mx_quantize(x)
+    with pytest.raises(ValueError):
+        mx_quantize(x.t())
+    with pytest.raises(TypeError):
+        mx_quantize(x.half())
+    with pytest.raises(B.MoEError):
+        mx_quantize(torch.zeros((4, 40), device="cuda"))
+    with pytest.raises(ValueError):
+        mx_dequantize(q, BF16, out=torch.empty((20, 64), device="cuda"))
+    with pytest.raises(B.MoEError):
+        mx_dequantize(MXTensor(q.data, q.scales[:100].clone()), BF16)
+    with pytest.raises(ValueError):
+        mx_matmul(q, MXTensor(w[0].data[0], w[0].scales[:100].clone()))
+    with pytest.raises(ValueError):
+        mx_matmul(q, w[0])  # one group against four
+    with pytest.raises(TypeError):
+        mx_matmul(x, w[0])
+    with pytest.raises(TypeError):
+        mx_experts(x, idx, gate, w[0], w[1], x)
+    with pytest.raises(ValueError):
+        mx_experts(x, idx.long(), gate, *w)
+    with pytest.raises(ValueError):
+        mx_experts(x, idx, gate, w[0], MXTensor(w[1].data[:, ::2], w[1].scales), w[2])
+    with pytest.raises(B.MoEError):
+        mx_experts(x, idx, gate, *w, workspace=torch.empty((256,), dtype=torch.uint8, device="cuda"))
+    assert int(device_status("cuda").item()) == 0
