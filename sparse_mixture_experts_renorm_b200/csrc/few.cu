@@ -19,7 +19,7 @@
 // kernel of its own would cost a launch: instead each cluster of few_up
 // computes all of it, its CTAs a part of the d columns each, exchanged
 // through distributed shared memory. Every cluster adds in the same order,
-// so all come to the same choices, and few_down takes them from topk_idx.
+// so all come to the same choices; few_down takes them from the workspace.
 //
 // A down product's rows of different experts belong to the same output: each
 // finished part is written to y, and the last of a block of 16 columns to
@@ -28,13 +28,14 @@
 // Measured (bf16, us and bytes that it cannot do without over the time): 16
 // tokens of the Mixtral-shaped layer (d 4096, I 14336, 8 experts, k 2) 422 us,
 // 6.6 TB/s; 5 tokens of the fine-grained one (d 2048, I 1408, 64 experts, k 6)
-// 77 us, 5.6 TB/s; one token of the small one (d 1024, I 2816, 8 experts, k 2)
-// 21 us, 1.6 TB/s. What is left there: some 8 us from the launch to the first
+// 76 us, 5.7 TB/s; one token of the small one (d 1024, I 2816, 8 experts, k 2)
+// 20 us, 1.7 TB/s. What is left there: some 8 us from the launch to the first
 // weight (3.6 us of logits, 2.5 us of choosing and 1.3 us of grouping for 64
 // experts; half of that for 8), 4 us between the kernels, and the last items'
 // and joins' tail.
 #include <atomic>
 #include <math.h>
+#include <stddef.h>
 
 #include "few_internal.h"
 #include "pair.cuh"
@@ -55,7 +56,7 @@ constexpr int kWeightBytes = kRows * kChunk;
 constexpr int kTokPitch = kFewTokPitch;  // bytes between token rows: two rows of a quarter-warp's load on different banks
 static_assert(kTokPitch == kChunk + 64, "pitch");
 constexpr int kMaxStages = 10;           // of a group
-constexpr int kAhead = 8;                // stages of a block brought to L2 ahead of time: 19 MB on 148 SMs
+constexpr int kAhead = 5;                // stages of a block brought to L2 ahead of time: 12 MB on 148 SMs
 constexpr int kJoinQueue = 256;          // items that the joins may lie behind the products
 constexpr int kMaxRows = kFewTokens * kMaxTopK;
 constexpr int kCluster = 4;              // CTAs that share one routing
@@ -72,9 +73,13 @@ struct Plan {
   int tj[kMaxRows];                 // t * k + j of a row
   int tok[kMaxRows];                // and t
   float gate[kMaxRows];
+  // what follows is not for few_down
   uint32_t mask[kMaxExperts];       // tokens of an expert
   int slot[kMaxExperts];
 };
+
+constexpr int kPlanWords = (int)(offsetof(Plan, mask) / 4);
+static_assert(kPlanWords <= kFewPlanWords, "the workspace's plan");
 
 // One group's barriers and lists.
 struct Group {
@@ -863,6 +868,8 @@ __device__ void consume_up(const FewArgs& a, Ctrl& c, Group& g, const Ring& ring
   }
 }
 
+__device__ __forceinline__ void fence_gpu() { asm volatile("fence.acq_rel.gpu;" ::: "memory"); }
+
 // Waits until `ready` says so, at most limit_ns; false: gave up.
 template <typename F>
 __device__ __forceinline__ bool poll(const FewArgs& a, Ctrl& c, F ready) {
@@ -902,7 +909,7 @@ __device__ void join(const FewArgs& a, Ctrl& c, Group& g, const Work<X, false>& 
     __syncwarp();
     const bool more = f >= 0;
     const int ready = more ? f : ~f;
-    __threadfence();
+    fence_gpu();
     while (done < ready) {
       const int n = min(32, ready - done);
       int blk = -1;
@@ -911,7 +918,7 @@ __device__ void join(const FewArgs& a, Ctrl& c, Group& g, const Work<X, false>& 
         if (atomicAdd(&a.done[blk], 1) != all - 1) blk = -1;
       }
       uint32_t last = __ballot_sync(0xffffffffu, blk >= 0);
-      __threadfence();
+      fence_gpu();
       while (last) {
         const int b = __shfl_sync(0xffffffffu, blk, __ffs(last) - 1);
         last &= last - 1;
@@ -1069,7 +1076,10 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(threads<X>(),
   choose(a, part, reinterpret_cast<uint32_t*>(scratch), *c, first);
   __syncthreads();
   make_plan<X>(a, c->plan, c->idx, c->gate);
-  if (first && (a.counts || a.aux)) statistics(a, part, *c);
+  if (first) {
+    for (int i = threadIdx.x; i < kPlanWords; i += blockDim.x) a.plan[i] = reinterpret_cast<const int32_t*>(&c->plan)[i];
+    if (a.counts || a.aux) statistics(a, part, *c);
+  }
   fence_async();  // the ring's memory was written above, and is next by the copies
   __syncthreads();
   stream<X, true>(maps, a, *c, ring, red);
@@ -1085,18 +1095,8 @@ __global__ void __launch_bounds__(threads<X>(), 1) few_down_kernel(const __grid_
   init_ctrl<X, false>(*c);
   pdl_wait();
   pdl_trigger();
-  const int i = threadIdx.x;
-  if (i < a.T * a.k) {
-    int e = a.idx[i];
-    if (e < 0 || e >= a.E) {  // few_up wrote them: something else has written there since
-      atomicOr(a.status, MOE_DEV_INTERNAL);
-      e = 0;
-    }
-    c->idx[i] = e;
-    c->gate[i] = a.gate[i];
-  }
+  for (int i = threadIdx.x; i < kPlanWords; i += blockDim.x) reinterpret_cast<int32_t*>(&c->plan)[i] = a.plan[i];
   __syncthreads();
-  make_plan<X>(a, c->plan, c->idx, c->gate);
   fence_async();  // few_up's hidden rows are read by the copies
   stream<X, false>(maps, a, *c, ring, red);
 }
@@ -1173,6 +1173,7 @@ FewWorkspace few_layout(int T, int d, int k, int I, moe_dtype dtype) {
   // of 16 columns do not go evenly into the SMs
   w.split = R > 0 && 256 / R < kFewMaxSplit ? (int)(256 / R) : kFewMaxSplit;
   size_t o = 0;
+  w.plan = o; o = align256(o + 4 * kFewPlanWords);
   w.next = o; o = align256(o + 4);
   w.done = o; o = align256(o + 4 * (size_t)((d + kRows - 1) / kRows));
   const size_t chunks = (el * (size_t)I + kChunk - 1) / kChunk;

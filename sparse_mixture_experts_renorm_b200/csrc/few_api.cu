@@ -62,6 +62,7 @@ moe_status moe_forward_few(const void* x, const void* w_router, const float* b_r
   a.x = x, a.wr = w_router, a.wg = w_gate, a.wu = w_up, a.wd = w_down, a.br = b_router;
   a.T = T, a.d = d, a.E = E, a.k = k, a.I = I, a.renorm = renorm;
   a.out = out, a.idx = topk_idx, a.gate = topk_gate, a.counts = counts, a.aux = aux;
+  a.plan = reinterpret_cast<int32_t*>(ws + l.plan);
   a.next = reinterpret_cast<int32_t*>(ws + l.next);
   a.done = reinterpret_cast<int32_t*>(ws + l.done);
   a.h = ws + l.h;

@@ -10,8 +10,11 @@ constexpr int kFewTokens = MOE_FEW_TOKENS;  // two n8 tiles of an mma.sync step
 constexpr int kFewMaxSplit = 8;                // parts of a down product's columns
 constexpr int kFewTokPitch = 1024 + 64;        // bytes between token rows in shared memory and of hidden rows
 
+constexpr int kFewPlanWords = 1024;
+
 // Byte offsets inside the workspace.
 struct FewWorkspace {
+  size_t plan;   // int32 [kFewPlanWords] the rows of every expert, from few_up to few_down
   size_t next;   // int32 [1] few_down's next item
   size_t done;   // int32 [blocks of 16 output columns] finished parts
   size_t h;      // hidden rows by expert and chunk of columns (few.cu, hidden_at)
@@ -29,6 +32,7 @@ struct FewArgs {
   float* gate;
   int32_t* counts;  // NULL: not wanted
   float* aux;       // NULL: not wanted
+  int32_t* plan;
   int32_t* next;
   int32_t* done;
   void* h;
