@@ -38,7 +38,7 @@
 // with zeros for codes it does not. A tile costs 0.9 us beside its products
 // (the last of them, the accumulator's way out, the first stage): 28 % for the
 // 8 stages of K = 2048. 32 rows through the Mixtral-shaped experts are bound by
-// the weights' bytes: 91 us gate/up, 50 us down, 5.5 and 5.0 TB/s.
+// the weights' bytes: gate/up 90 us, 5.5 TB/s.
 #include "mx.cuh"
 #include "mx_internal.h"
 #include "mx_umma.cuh"
@@ -440,7 +440,10 @@ cudaError_t launch(const MxMaps& m, const int32_t* offsets, int G, int M, int N,
 
 cudaError_t launch_mx_product(const MxMaps& m, const int32_t* offsets, int G, int M, int N, int K, int group_tiles,
                               const MxOut& out, int32_t* status, cudaStream_t stream) {
-  if ((long long)M <= (offsets ? 128ll * G : 128ll))
+  // 64 groups of N 1408, K 2048, us there and here: 8 rows each on average 20.6
+  // and 22.7, 32 rows 22.0 and 24.1, 64 rows 24.9 and 26.0, 96 rows 27.5 and 27.5,
+  // 128 rows 30.6 and 28.1
+  if ((long long)M <= (offsets ? 64ll * G : 64ll))
     return launch_mx_product_rows(m, offsets, G, M, N, K, group_tiles, out, status, stream);
   if (out.form == kMxY16) return launch<kMxY16>(m, offsets, G, M, N, K, group_tiles, out, status, stream);
   if (out.form == kMxF32) return launch<kMxF32>(m, offsets, G, M, N, K, group_tiles, out, status, stream);

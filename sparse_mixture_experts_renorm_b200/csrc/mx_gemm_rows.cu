@@ -13,7 +13,10 @@
 // 128 columns at most, so there are two, and the epilogue runs beside the next
 // tile's products. 26 KB a stage, 8 stages; otherwise as there.
 //
-// Taken where groups have at most 128 rows on average.
+// Taken where groups have at most 64 rows on average (mx_gemm.cu has both sides
+// measured: with more, twice the tiles and stores of single columns cost what
+// the rows save). Bound by the weights' bytes: 64 rows over 8 groups of 4096 x
+// 14336 in 40 us, 6.3 TB/s.
 #include "mx_umma.cuh"
 
 namespace moe {

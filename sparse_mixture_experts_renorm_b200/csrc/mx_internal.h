@@ -46,7 +46,7 @@ struct MxOut {
 // group, group_tiles: tile rows of scales per weight group.
 cudaError_t launch_mx_product(const MxMaps& m, const int32_t* offsets, int G, int M, int N, int K, int group_tiles,
                               const MxOut& out, int32_t* status, cudaStream_t stream);
-// The same for groups of few rows (at most 128 on average: mx_gemm_rows.cu).
+// The same for groups of few rows (mx_gemm_rows.cu); launch_mx_product takes it by itself.
 cudaError_t launch_mx_product_rows(const MxMaps& m, const int32_t* offsets, int G, int M, int N, int K, int group_tiles,
                                    const MxOut& out, int32_t* status, cudaStream_t stream);
 // H[r] = MXFP4(SiLU(A[r] . B0[g]^T) * (A[r] . B1[g]^T)), N hidden units.

@@ -158,7 +158,11 @@ def test_product_dense_groups(G, M, N, K):
 
 @pytest.mark.parametrize("offsets,M,N,K", [([0, 7], 7, 40, 64), ([0, 0, 1, 1, 258, 770, 770], 780, 264, 352),
                                            ([0, 300, 556], 556, 256, 512), ([5, 5, 6, 200], 260, 72, 288),
-                                           ([0] * 128 + [3] * 128 + [9], 9, 64, 96), ([0, 0, 0], 4, 64, 64)])
+                                           ([0] * 128 + [3] * 128 + [9], 9, 64, 96), ([0, 0, 0], 4, 64, 64),
+                                           # few rows on average, one group with more than a tile of them
+                                           ([0] * 20 + [1, 290, 290, 291, 400, 403], 403, 264, 1056), ([2, 66], 70, 520, 224),
+                                           # many
+                                           ([0, 130, 131, 520], 530, 72, 544)])
 def test_product_ragged(offsets, M, N, K):
     G = len(offsets) - 1
     off = torch.tensor(offsets, dtype=torch.int32, device="cuda")
