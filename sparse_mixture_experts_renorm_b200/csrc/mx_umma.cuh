@@ -56,8 +56,12 @@ __device__ __forceinline__ float max_abs_nan(float a, float b) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(fabsf(b)));
   return m;
 }
+
+// A tile of the grouped product. The rows of A's tiles are the caller's: s_mt
+// holds the tiles before each group, s_off its first row; the tiles of one
+// weight block follow each other.
 struct MxTile {
-  int g, m, n, row0, cnt;  // group, 256-row tile, weight block, first row and rows of the group
+  int g, m, n, row0, cnt;  // group, its tile of rows, weight block, first row and rows of the group
 };
 
 __device__ __forceinline__ MxTile mx_tile(int tile, int n_wb, const int* s_off, const int* s_mt, int G) {
