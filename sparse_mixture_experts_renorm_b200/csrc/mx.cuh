@@ -174,16 +174,22 @@ struct Piece<float> {
 
 // Rows of expert outputs between the down product and the sum over a token's
 // experts: fp16 with one exponent byte per 32 columns, by which the largest of
-// them lies in [1, 2). That leaves 2^-11 of a value where bf16 would leave
-// 2^-8, half the error of the whole layer, for the same bytes. Exponent byte
-// 0xFF: the block holds a NaN or an infinity, and its columns are bf16.
+// them lies in [1, 2), or in [2, 4) from 2^127 on (254 would need 2^-127, which
+// is no normal number; fp16 holds 4 as well as 2). That leaves 2^-11 of a value
+// where bf16 would leave 2^-8, half the error of the whole layer, for the same
+// bytes. Exponent byte 0xFF: the block holds a NaN or an infinity, and its
+// columns are bf16.
 // Exponent bytes stand by 256 columns and rows, eight for each.
 __host__ __device__ __forceinline__ size_t y16_exp_at(size_t rows, int col, size_t row) {
   return ((size_t)(col >> 8) * rows + row) * 8 + ((col >> 5) & 7);
 }
-__device__ __forceinline__ uint32_t y16_exp(uint32_t amax_bits) { return max(amax_bits >> 23, 1u); }
-__device__ __forceinline__ float y16_inv(uint32_t e) { return __uint_as_float((254u - e) << 23); }  // 2^(127 - e)
-__device__ __forceinline__ float y16_step(uint32_t e) { return __uint_as_float(e << 23); }          // 2^(e - 127)
+__device__ __forceinline__ uint32_t y16_exp(uint32_t amax_bits) {
+  const uint32_t e = amax_bits >> 23;
+  return e == 0xffu ? e : min(max(e, 1u), 253u);
+}
+// For exponents 1 .. 253: 2^(127 - e) and 2^(e - 127).
+__device__ __forceinline__ float y16_inv(uint32_t e) { return __uint_as_float((254u - e) << 23); }
+__device__ __forceinline__ float y16_step(uint32_t e) { return __uint_as_float(e << 23); }
 __device__ __forceinline__ uint32_t y16_pack(float a, float b, float inv) {
   const __half2 h = __floats2half2_rn(a * inv, b * inv);
   return *reinterpret_cast<const uint32_t*>(&h);
