@@ -825,8 +825,12 @@ __device__ __forceinline__ void put4(__nv_bfloat16* p, const float4& v) {
 }
 __device__ __forceinline__ void put4(float* p, const float4& v) { *reinterpret_cast<float4*>(p) = v; }
 // A hidden value into its row, and what the row leaves of it into the next.
+// The first term is held to bf16's largest number, so that a value between that
+// and fp32's largest keeps its rest (infinity minus infinity is none), and an
+// infinite value or a NaN is the second term alone.
 __device__ __forceinline__ void put_hidden(uint8_t* p, float v, const __nv_bfloat16*) {
-  const __nv_bfloat16 hi = __float2bfloat16_rn(v);
+  constexpr float kMost = 3.38953139e38f;  // (2 - 2^-7) 2^127
+  const __nv_bfloat16 hi = __float2bfloat16_rn(fminf(fmaxf(v, -kMost), kMost));
   *reinterpret_cast<__nv_bfloat16*>(p) = hi;
   *reinterpret_cast<__nv_bfloat16*>(p + kTokPitch) = __float2bfloat16_rn(v - __bfloat162float(hi));
 }

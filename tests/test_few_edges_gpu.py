@@ -1,0 +1,44 @@
+"""moe_forward_few where its numbers, its queues and its callers come to their
+ends; test_few_gpu.py derives the tolerances."""
+import numpy as np
+import pytest
+import torch
+
+from sparse_mixture_experts_renorm_b200 import moe_forward_few
+from test_few_gpu import BF16, F32, f64
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T", [1, 5])
+def test_hidden_values_at_the_end_of_the_range(T, dtype):
+    """Hidden unit i is SiLU(g_i) u_i of one column of x: exactly g_i u_i, as SiLU(90.5) is 90.5 in fp32 (e^-90.5 is
+    below 2^-130). 181 * 181 has 15 bits, so 181^2 2^113, 1.9996 * 2^127, is an fp32 number between the largest of
+    bf16 and that of fp32; twice that is infinite in fp32. Other tokens' outputs are zeros."""
+    d = I = 64
+    units = np.zeros(I)
+    units[[3, 20, 41, 63]] = 181.0 * 2.0**114, -181.0 * 2.0**114, 181.0 * 2.0**113, 255.0 * 2.0**113
+    down = torch.randn((1, d, I), generator=torch.Generator().manual_seed(1)).mul(2.0**-20).to(dtype)
+    p = {"x": torch.zeros((T, d)), "w_router": torch.zeros((1, d)), "w_gate": torch.zeros((1, I, d)),
+         "w_up": torch.zeros((1, I, d)), "w_down": down}
+    p["x"][T - 1, 7] = 1
+    p["w_gate"][0, :, 7] = 90.5
+    p["w_up"][0, :, 7] = torch.tensor(units, dtype=F32)
+    p = {n: v.to(dtype).cuda() for n, v in p.items()}
+    r = moe_forward_few(**p, b_router=None, k=1, renorm=True)
+    h = 90.5 * units
+    assert 3.3895e38 < h[3] < 3.4028e38 and np.array_equal(f64(p["w_up"])[0, :, 7], units)
+    want, mag = f64(down)[0] @ h, np.abs(f64(down)[0]) @ np.abs(h)
+    # SiLU 2^-18 of the value, two bf16 terms 2^-16 (none of both in fp32, where it is 2^-20), the sum, the output
+    tol = mag * ((2.0**-18 + 2.0**-16 if dtype == BF16 else 2.0**-20) + (I + 8) * 2.0**-23)
+    tol += (2.0**-8 if dtype == BF16 else 2.0**-24) * (np.abs(want) + tol)
+    assert (np.abs(f64(r.out[T - 1]) - want) <= tol).all()
+    assert (r.out[:T - 1] == 0).all()
+
+    p["w_up"][0, 3, 7] = 181.0 * 2.0**115  # and a unit that is infinite: so is every output it takes part in
+    p["w_up"][0, 20, 7] = 0
+    r = moe_forward_few(**p, b_router=None, k=1, renorm=True)
+    w = down[0, :, 3].float().cuda()
+    assert (w != 0).all() and torch.equal(r.out[T - 1].float(), torch.sign(w) * float("inf"))
+    assert (r.out[:T - 1] == 0).all()
