@@ -55,6 +55,11 @@ moe_status check_matrix(int groups, long long rows, int cols, const char* what) 
   return MOE_OK;
 }
 
+// The same with offsets: `rows` are those of all groups together.
+moe_status check_ragged(int groups, long long rows, int cols, const char* what) {
+  return groups <= 0 ? check_matrix(groups, 1, cols, what) : check_matrix(1, rows, cols, what);
+}
+
 moe_status check_mx_shape(int T, int d, int E, int k, int I) {
   moe_status st = check_shape(T, 64, E, k, 64, MOE_BF16);  // T, E and k as for the layer
   if (st != MOE_OK) return st;
@@ -201,7 +206,7 @@ moe_status mx_layer(const void* x, const void* w_router, const float* b_router, 
 extern "C" {
 
 size_t moe_mx_scale_bytes(int groups, int rows, int cols, int ragged) {
-  if (check_matrix(groups, rows, cols, "moe_mx_scale_bytes") != MOE_OK) return 0;
+  if ((ragged ? check_ragged : check_matrix)(groups, rows, cols, "moe_mx_scale_bytes") != MOE_OK) return 0;
   const long long tiles = ragged ? 2 * ((long long)rows / 256 + (rows < groups ? rows : groups))
                                  : groups * mx_group_tiles(rows);
   return (size_t)(tiles > 2 ? tiles : 2) * mx_stage_count(cols) * 1024;
@@ -211,12 +216,12 @@ static moe_status convert_args(const void* a, const void* data, const void* scal
                                const int32_t* offsets, int groups, int rows, int cols, moe_dtype dtype,
                                size_t* tile_rows, const char* what) {
   if (dtype != MOE_F32 && dtype != MOE_BF16) return fail(MOE_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
-  moe_status st = check_matrix(groups, offsets ? 1 : rows, cols, what);
-  if (st == MOE_OK && offsets) st = check_matrix(1, rows, cols, what);
+  const moe_status st = (offsets ? check_ragged : check_matrix)(groups, rows, cols, what);
   if (st != MOE_OK) return st;
   if (offsets && groups > kMaxExperts)
     return fail(MOE_ERR_UNSUPPORTED, "%s: at most %d groups of rows with offsets (got %d)", what, kMaxExperts, groups);
-  const size_t need = moe_mx_scale_bytes(groups, rows, cols, offsets != nullptr);
+  const size_t need = moe_mx_scale_bytes(groups, rows, cols, offsets != nullptr);  // not 0: the sizes are valid
+  if (need == 0) return MOE_ERR_INVALID_ARG;
   if (scale_bytes < need)
     return fail(MOE_ERR_INVALID_ARG, "%s: the scales need %zu bytes (got %zu)", what, need, scale_bytes);
   if (rows > 0) {
@@ -259,7 +264,7 @@ moe_status moe_mx_matmul(const void* a, const void* a_scales, const void* b, con
                          int32_t* status_dev, void* stream) {
   if (out_dtype != MOE_F32 && out_dtype != MOE_BF16)
     return fail(MOE_ERR_INVALID_ARG, "unknown output dtype %d", (int)out_dtype);
-  moe_status st = check_matrix(offsets ? 1 : groups, M, K, "moe_mx_matmul (A)");
+  moe_status st = (offsets ? check_ragged : check_matrix)(groups, M, K, "moe_mx_matmul (A)");
   if (st == MOE_OK) st = check_matrix(groups, N, K, "moe_mx_matmul (B)");
   if (st != MOE_OK) return st;
   if (N <= 0) return fail(MOE_ERR_INVALID_ARG, "N must be positive (got %d)", N);
