@@ -422,8 +422,9 @@ moe_status moe_mx_dequantize(const void* data, const void* scales, size_t scale_
  * moe_mx_matmul — out[r, :] = A[r] . B[g]^T for the rows r of every group g:
  * A [groups, M, K] (offsets NULL) or [M, K] with offsets, B [groups, N, K]
  * dense, both MXFP4, out [rows of A, N] fp32 or bf16. Products and sums in
- * fp32, rounded once. N % 8 == 0, groups <= 256. Rows of no group are left as
- * they were. The scales of A and B hold moe_mx_scale_bytes() bytes.
+ * fp32, rounded once. N % 8 == 0, groups <= 256, at most 2^31 - 256 rows of A
+ * and of B. Rows of no group are left as they were. The scales of A and B hold
+ * moe_mx_scale_bytes() bytes.
  * status_dev: device int32 [1], required: MOE_DEV_INTERNAL is OR-ed in and
  * nothing computed when the offsets are not a partition (negative, decreasing
  * or past M).
@@ -438,7 +439,8 @@ moe_status moe_mx_matmul(const void* a, const void* a_scales, const void* b, con
  * and the SwiGLU hidden rows are rounded to MXFP4 from fp32 between them. Each
  * expert row times its gate is rounded to 2^-11 of a value (2^-25 of the
  * largest of its 32 columns where that is more), a token's rows are added in slot order in fp32, and out
- * [T, d] is bf16. d % 32 == 0 and I % 32 == 0.
+ * [T, d] is bf16. d % 32 == 0 and I % 32 == 0; E I, E d and T k at most
+ * 2^31 - 256, d I below 2^31.
  *
  * moe_mx_experts takes the choices and gates: topk_idx [T, k], any experts
  * (the same one twice is two assignments), topk_gate [T, k] any values. A

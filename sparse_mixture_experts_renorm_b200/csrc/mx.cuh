@@ -21,7 +21,9 @@ constexpr int kMxTileRows = 128;
 constexpr int kMxStageCols = 256;
 constexpr int kMxStageBytes = 1024;  // scales of 128 rows x 256 columns
 
-__host__ __device__ __forceinline__ int mx_stages(int cols) { return (cols + kMxStageCols - 1) / kMxStageCols; }
+__host__ __device__ __forceinline__ int mx_stages(int cols) {
+  return (int)(((unsigned)cols + kMxStageCols - 1) / kMxStageCols);
+}
 
 // Byte of the scale of (tile row, row r < 128 of it, block b of the row).
 __host__ __device__ __forceinline__ size_t mx_scale_at(size_t tile_row, int stages, int r, int b) {

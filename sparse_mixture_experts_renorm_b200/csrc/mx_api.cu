@@ -11,6 +11,8 @@ using namespace moe;
 namespace {
 
 constexpr long long kIntMax = (1ll << 31) - 1;
+// Rows of a product's operands: the end of a tile of 256 is an int as well.
+constexpr long long kProductRows = kIntMax - 255;
 
 // Byte offsets inside the workspace of the experts.
 struct MxWorkspace {
@@ -66,8 +68,9 @@ moe_status check_mx_shape(int T, int d, int E, int k, int I) {
   if (d <= 0 || I <= 0) return fail(MOE_ERR_INVALID_ARG, "d and I must be positive (got d=%d I=%d)", d, I);
   if (d % 32 != 0 || I % 32 != 0)
     return fail(MOE_ERR_UNSUPPORTED, "MXFP4 experts need d %% 32 == 0 and I %% 32 == 0 (got d=%d I=%d)", d, I);
-  if ((long long)d * I > kIntMax || (long long)E * I > kIntMax || (long long)E * d > kIntMax)
-    return fail(MOE_ERR_UNSUPPORTED, "d*I, E*I and E*d must be < 2^31");
+  if ((long long)d * I > kIntMax || (long long)E * I > kProductRows || (long long)E * d > kProductRows ||
+      (long long)T * k > kProductRows)
+    return fail(MOE_ERR_UNSUPPORTED, "d*I must be < 2^31, and E*I, E*d and T*k at most 2^31 - 256");
   return MOE_OK;
 }
 
@@ -275,7 +278,8 @@ moe_status moe_mx_matmul(const void* a, const void* a_scales, const void* b, con
       offsets ? 2 * ((long long)M / 256 + (M < groups ? M : groups)) : groups * mx_group_tiles(M);
   const long long b_tiles = groups * mx_group_tiles(N);
   const int stages = mx_stage_count(K);
-  if (a_tiles * stages > kIntMax || b_tiles * stages > kIntMax || (a_tiles / 2) * ((N + 255) / 256) > kIntMax)
+  if ((offsets ? 1ll : (long long)groups) * M > kProductRows || (long long)groups * N > kProductRows ||
+      a_tiles * stages > kIntMax || b_tiles * stages > kIntMax || (a_tiles / 2) * ((N + 255) / 256) > kIntMax)
     return fail(MOE_ERR_UNSUPPORTED, "the product is too large for one call");
   if (M == 0) return MOE_OK;
   if (!a || !a_scales || !b || !b_scales || !out || !status_dev)

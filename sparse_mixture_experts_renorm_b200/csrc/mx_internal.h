@@ -9,7 +9,7 @@ namespace moe {
 // starts at a new pair of tiles).
 inline long long mx_group_tiles(long long rows) { return (rows + 255) / 256 * 2; }
 // Pieces of 256 columns (one pipeline stage of the product) of a row.
-inline int mx_stage_count(int cols) { return (cols + 255) / 256; }
+inline int mx_stage_count(int cols) { return (int)(((unsigned)cols + 255) / 256); }
 
 // Rows to MXFP4 and back. offsets == NULL: x is [n_rows / rows, rows, cols],
 // every group padded to group_tiles tile rows of scales; otherwise x is

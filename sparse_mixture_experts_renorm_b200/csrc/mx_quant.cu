@@ -37,7 +37,7 @@ __device__ __forceinline__ void load_groups(Groups& s, const int32_t* __restrict
   const int g = threadIdx.x, lane = g & 31, w = g >> 5;
   const int a = g <= G ? offsets[g] : 0;
   const int b = g < G ? offsets[g + 1] : a;
-  const int tiles = b > a ? ((b - a + 255) >> 8) * 2 : 0;
+  const int tiles = b > a ? (int)(((unsigned)(b - a) + 255u) >> 8) * 2 : 0;
   int incl = tiles;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
