@@ -1062,6 +1062,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(threads<X>(),
   float* part = reinterpret_cast<float*>(ring);                     // [kCluster][T][E]
   float* scratch = part + (size_t)kCluster * a.T * a.E;             // [kWarps][16][kPassLd]
   const int rank = (int)cluster_ctarank();
+  __syncwarp();    // single threads of warps 0 and 1 were at work, and the barrier's instructions take whole warps
   cluster_sync();  // the peers' shared memory exists
   pdl_wait();
   pdl_trigger();

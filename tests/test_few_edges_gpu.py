@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from sparse_mixture_experts_renorm_b200 import moe_forward_few
-from test_few_gpu import BF16, F32, f64
+from test_few_gpu import BF16, F32, check_out, check_routing, f64, layer
 
 pytestmark = pytest.mark.gpu
 
@@ -42,3 +42,16 @@ def test_hidden_values_at_the_end_of_the_range(T, dtype):
     w = down[0, :, 3].float().cuda()
     assert (w != 0).all() and torch.equal(r.out[T - 1].float(), torch.sign(w) * float("inf"))
     assert (r.out[:T - 1] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_calls_with_and_without_weights_asked_for_ahead(dtype):
+    """One warp of a block asks for the experts' weights ahead of the routing where nearly all of them will be chosen
+    (16 tokens, 4 experts of 6; not for 2 tokens and one), while another sets up the barriers: in turn, on one stream."""
+    p, q = layer(16, 1032, 6, 4, 264, 50, dtype), layer(2, 1032, 6, 1, 264, 51, dtype)
+    want = [moe_forward_few(**v, k=k, renorm=True) for v, k in ((p, 4), (q, 1))]
+    for v, k, r in ((p, 4, want[0]), (q, 1, want[1])):
+        check_routing(v, k, True, r.topk_idx, r.topk_gate)
+        check_out(v, r.topk_idx, r.topk_gate, r.out, dtype)
+    got = [[moe_forward_few(**v, k=k, renorm=True).out for v, k in ((p, 4), (q, 1))] for _ in range(100)]
+    assert all(torch.equal(a, want[0].out) and torch.equal(b, want[1].out) for a, b in got)
