@@ -910,6 +910,9 @@ __device__ void join(const FewArgs& a, Ctrl& c, Group& g, const Work<X, false>& 
       });
     if (!__all_sync(0xffffffffu, ok)) return;
     f = __shfl_sync(0xffffffffu, f, 0);
+    // what lane 0 saw finished, the other lanes count: its read is ordered in
+    // front of the warp's barrier, and their atomics behind a fence
+    if (lane == 0) __threadfence_block();
     __syncwarp();
     const bool more = f >= 0;
     const int ready = more ? f : ~f;
@@ -922,7 +925,10 @@ __device__ void join(const FewArgs& a, Ctrl& c, Group& g, const Work<X, false>& 
         if (atomicAdd(&a.done[blk], 1) != all - 1) blk = -1;
       }
       uint32_t last = __ballot_sync(0xffffffffu, blk >= 0);
+      // the parts are read by other lanes than the one whose atomic was the
+      // last: it fences, and the warp's barrier hands that on
       fence_gpu();
+      __syncwarp();
       while (last) {
         const int b = __shfl_sync(0xffffffffu, blk, __ffs(last) - 1);
         last &= last - 1;

@@ -55,3 +55,24 @@ def test_calls_with_and_without_weights_asked_for_ahead(dtype):
         check_out(v, r.topk_idx, r.topk_gate, r.out, dtype)
     got = [[moe_forward_few(**v, k=k, renorm=True).out for v, k in ((p, 4), (q, 1))] for _ in range(100)]
     assert all(torch.equal(a, want[0].out) and torch.equal(b, want[1].out) for a, b in got)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_many_more_items_than_the_joins_may_lie_behind(dtype):
+    """Token t chooses experts 8t .. 8t + 7, so that 128 experts have a token each: 128 * 2048 items of 16 output
+    columns, on average at least three times the 256 that a pipeline's joins may lie behind its products (two
+    pipelines a block in bf16), so that each one's queue goes round."""
+    T, E, k, d, I = 16, 128, 8, 32768, 8
+    pipelines = 2 * torch.cuda.get_device_properties(0).multi_processor_count
+    assert E * (d // 16) > 3 * 256 * pipelines
+    p = layer(T, d, E, k, I, 52, dtype, bias=False)
+    p["w_router"].zero_()
+    p["x"][:, :T] = torch.eye(T, device="cuda").to(dtype)
+    e = torch.arange(E, device="cuda")
+    p["w_router"][e, e // 8] = (8 + (e % 8) / 2).to(dtype)
+    r = moe_forward_few(**p, k=k, renorm=True)
+    assert torch.equal(r.topk_idx.long(), e.view(T, k).flip(1))
+    check_routing(p, k, True, r.topk_idx, r.topk_gate, ties=True)
+    check_out(p, r.topk_idx, r.topk_gate, r.out, dtype)
+    for _ in range(5):
+        assert torch.equal(r.out, moe_forward_few(**p, k=k, renorm=True).out)
