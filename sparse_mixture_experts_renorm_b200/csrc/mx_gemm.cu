@@ -332,7 +332,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
       tmem_ld_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster_cta(tempty_leader);
+      if (lane == 0) mbar_arrive_cluster_relaxed(tempty_leader);
       if (first >= t.cnt) continue;  // none of them exists
       if (kGateUp) {
         const int unit0 = t.n * 128 + part * 32;

@@ -263,7 +263,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster_cta(map_to_cta(&tempty[acc], 0));
+      if (lane == 0) mbar_arrive_cluster_relaxed(map_to_cta(&tempty[acc], 0));
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1u;
       const int col0 = t.n * 256 + (int)rank * 128 + q * 32, col = col0 + lane;

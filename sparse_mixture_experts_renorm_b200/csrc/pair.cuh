@@ -34,11 +34,13 @@ __device__ __forceinline__ uint32_t map_to_cta(const void* p, uint32_t rank) {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
-// The same without ordering this thread's global stores for the cluster, which
-// the arrival above waits for (0.9 us behind an epilogue's): for reads that are
-// complete, such as TMEM loads that were waited for.
-__device__ __forceinline__ void mbar_arrive_cluster_cta(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+// Hands TMEM that was read back to another CTA's issuing thread. Relaxed: the
+// accumulator's reads are ordered by tcgen05.wait::ld and the fence in front of
+// the arrival (tc_fence_before) and the one behind the wait (tc_fence_after),
+// and nothing else is handed over. A release for the cluster would also wait
+// for this thread's global stores, 0.9 us behind an epilogue's.
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 // TMA tile load into this CTA's shared memory whose completion is counted on
 // the barrier at `bar_cluster` (the leading CTA's).
