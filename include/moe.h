@@ -367,7 +367,9 @@ moe_status moe_pipeline_destroy(moe_pipeline* p);
  *   out         [T, d] in `dtype`: a token's expert outputs are added in fp32
  *               in slot order and rounded once
  *   counts, aux may be NULL: they are then not computed
- *   status_dev  device int32 [1], required (MOE_DEV_* bits are OR-ed in)
+ *   status_dev  device int32 [1], required (MOE_DEV_* bits are OR-ed in); or the
+ *               workspace, whose first four bytes are then this call's own word,
+ *               cleared by the call
  *   workspace   moe_few_workspace_size() bytes, 256-byte aligned, any contents;
  *               calls that overlap on the GPU need one each
  * MOE_BF16: d % 8 == 0 and I % 8 == 0; MOE_F32: d % 4 == 0 and I % 4 == 0.

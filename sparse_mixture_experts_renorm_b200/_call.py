@@ -1,5 +1,5 @@
 """What the wrappers of the newer entry points share: argument checks, the
-stream and device of a call, and the status word of calls without one."""
+stream and device of a call, and the status word of calls that return none."""
 from __future__ import annotations
 
 import contextlib
@@ -78,9 +78,11 @@ class on:
 
 
 def device_status(dev) -> torch.Tensor:
-    """The status word ([1] int32) that calls on this device without one of
-    their own OR their MOE_DEV_* bits into. Read it after synchronising; the
-    caller clears it."""
+    """The status word ([1] int32) of a device, into which ``mx_matmul`` calls
+    that are given none OR their MOE_DEV_* bits, on every stream and thread: it
+    says that some call since it was last cleared had a fault, not which one.
+    Read it after synchronising; the caller clears it. The first use on a device
+    makes it and cannot be captured into a graph."""
     if not isinstance(dev, torch.device):
         dev = torch.device(dev)
     i = torch.cuda.current_device() if dev.index is None else dev.index

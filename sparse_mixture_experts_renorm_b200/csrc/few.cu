@@ -79,7 +79,7 @@ struct Plan {
 };
 
 constexpr int kPlanWords = (int)(offsetof(Plan, mask) / 4);
-static_assert(kPlanWords <= kFewPlanWords, "the workspace's plan");
+static_assert(kPlanWords <= kFewPlanWords && kFewPlanAt + kFewPlanWords <= kFewUpAt, "the workspace's head");
 
 // One group's barriers and lists.
 struct Group {
@@ -1072,6 +1072,10 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(threads<X>(),
   cluster_sync();  // the peers' shared memory exists
   pdl_wait();
   pdl_trigger();
+  if (a.own && threadIdx.x == 0) {
+    a.head[kFewUpAt + blockIdx.x] = 0;
+    if (blockIdx.x == 0) atomicExch(a.status, 0);
+  }
   if (blockIdx.x == 0) {  // few_down counts on zeros
     for (int i = threadIdx.x; i < (a.d + kRows - 1) / kRows; i += blockDim.x) a.done[i] = 0;
     if (threadIdx.x == 0) *a.next = 0;
@@ -1088,12 +1092,13 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(threads<X>(),
   __syncthreads();
   make_plan<X>(a, c->plan, c->idx, c->gate);
   if (first) {
-    for (int i = threadIdx.x; i < kPlanWords; i += blockDim.x) a.plan[i] = reinterpret_cast<const int32_t*>(&c->plan)[i];
+    for (int i = threadIdx.x; i < kPlanWords; i += blockDim.x) a.head[kFewPlanAt + i] = reinterpret_cast<const int32_t*>(&c->plan)[i];
     if (a.counts || a.aux) statistics(a, part, *c);
   }
   fence_async();  // the ring's memory was written above, and is next by the copies
   __syncthreads();
   stream<X, true>(maps, a, *c, ring, red);
+  if (a.own && c->abort) atomicOr(&a.head[kFewUpAt + blockIdx.x], MOE_DEV_TIMEOUT);  // who gave up sees its own mark
 }
 
 template <typename X>
@@ -1106,7 +1111,10 @@ __global__ void __launch_bounds__(threads<X>(), 1) few_down_kernel(const __grid_
   init_ctrl<X, false>(*c);
   pdl_wait();
   pdl_trigger();
-  for (int i = threadIdx.x; i < kPlanWords; i += blockDim.x) reinterpret_cast<int32_t*>(&c->plan)[i] = a.plan[i];
+  static_assert(kFewUpWords <= threads<X>(), "a thread for each of few_up's words");
+  if (blockIdx.x == 0 && (int)threadIdx.x < a.own)  // few_up's status bits
+    if (const int bits = a.head[kFewUpAt + threadIdx.x]) atomicOr(a.status, bits);
+  for (int i = threadIdx.x; i < kPlanWords; i += blockDim.x) reinterpret_cast<int32_t*>(&c->plan)[i] = a.head[kFewPlanAt + i];
   __syncthreads();
   fence_async();  // few_up's hidden rows are read by the copies
   stream<X, false>(maps, a, *c, ring, red);
@@ -1170,7 +1178,10 @@ cudaError_t launch(const FewMaps& m, FewArgs a, cudaStream_t stream) {
   double out = 1.0;
   for (int t = 0; t < a.T; ++t) out *= 1.0 - (double)a.k / a.E;
   a.likely = out < 0.05;
-  err = launch_pdl(few_up_kernel<X>, dim3(dev.clusters * kCluster), dim3(threads<X>()), kSmemTotal, stream, m, a);
+  const int up_blocks = dev.clusters * kCluster;
+  if (up_blocks > kFewUpWords) return cudaErrorInvalidConfiguration;
+  if (a.own) a.own = up_blocks;
+  err = launch_pdl(few_up_kernel<X>, dim3(up_blocks), dim3(threads<X>()), kSmemTotal, stream, m, a);
   if (err != cudaSuccess) return err;
   return launch_pdl(few_down_kernel<X>, dim3(dev.sms), dim3(threads<X>()), kSmemTotal, stream, m, a);
 }
@@ -1184,7 +1195,7 @@ FewWorkspace few_layout(int T, int d, int k, int I, moe_dtype dtype) {
   // of 16 columns do not go evenly into the SMs
   w.split = R > 0 && 256 / R < kFewMaxSplit ? (int)(256 / R) : kFewMaxSplit;
   size_t o = 0;
-  w.plan = o; o = align256(o + 4 * kFewPlanWords);
+  w.head = o; o = align256(o + 4 * (kFewUpAt + kFewUpWords));
   w.next = o; o = align256(o + 4);
   w.done = o; o = align256(o + 4 * (size_t)((d + kRows - 1) / kRows));
   const size_t chunks = (el * (size_t)I + kChunk - 1) / kChunk;

@@ -41,9 +41,13 @@ moe_status moe_forward_few(const void* x, const void* w_router, const float* b_r
   if (renorm != 0 && renorm != 1) return fail(MOE_ERR_INVALID_ARG, "renorm must be 0 or 1 (got %d)", renorm);
   cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
   if (T == 0) {
+    if (status_dev && status_dev == workspace && workspace_bytes < sizeof(int32_t))
+      return fail(MOE_ERR_WORKSPACE, "the workspace has no room for the call's status word (%zu bytes)", workspace_bytes);
     cudaError_t err = counts ? cudaMemsetAsync(counts, 0, sizeof(int32_t) * E, stream) : cudaSuccess;
     if (err == cudaSuccess && aux) err = cudaMemsetAsync(aux, 0, sizeof(float), stream);
-    return err == cudaSuccess ? MOE_OK : fail_cuda(err, "zeroing counts and the statistic for T=0");
+    if (err == cudaSuccess && status_dev && status_dev == workspace)
+      err = cudaMemsetAsync(status_dev, 0, sizeof(int32_t), stream);
+    return err == cudaSuccess ? MOE_OK : fail_cuda(err, "zeroing counts, the statistic and the status word for T=0");
   }
   if (!x || !w_router || !w_gate || !w_up || !w_down || !out || !topk_idx || !topk_gate || !status_dev)
     return fail(MOE_ERR_INVALID_ARG,
@@ -62,13 +66,14 @@ moe_status moe_forward_few(const void* x, const void* w_router, const float* b_r
   a.x = x, a.wr = w_router, a.wg = w_gate, a.wu = w_up, a.wd = w_down, a.br = b_router;
   a.T = T, a.d = d, a.E = E, a.k = k, a.I = I, a.renorm = renorm;
   a.out = out, a.idx = topk_idx, a.gate = topk_gate, a.counts = counts, a.aux = aux;
-  a.plan = reinterpret_cast<int32_t*>(ws + l.plan);
+  a.head = reinterpret_cast<int32_t*>(ws + l.head);
   a.next = reinterpret_cast<int32_t*>(ws + l.next);
   a.done = reinterpret_cast<int32_t*>(ws + l.done);
   a.h = ws + l.h;
   a.y = reinterpret_cast<float*>(ws + l.y);
   a.split = l.split;
   a.status = status_dev;
+  a.own = status_dev == workspace;
   a.limit_ns = kWaitLimitNs;
   FewMaps m;
   if (!make_tmap_few(&m.wg, w_gate, dtype, (uint64_t)E * I, (uint64_t)d, 8) ||

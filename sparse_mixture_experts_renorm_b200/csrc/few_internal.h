@@ -10,11 +10,13 @@ constexpr int kFewTokens = MOE_FEW_TOKENS;  // two n8 tiles of an mma.sync step
 constexpr int kFewMaxSplit = 8;                // parts of a down product's columns
 constexpr int kFewTokPitch = 1024 + 64;        // bytes between token rows in shared memory and of hidden rows
 
-constexpr int kFewPlanWords = 1024;
+// The workspace's first words: the call's status word, the plan from few_up to
+// few_down, and a status word of each of few_up's blocks.
+constexpr int kFewPlanAt = 4, kFewPlanWords = 764, kFewUpAt = 768, kFewUpWords = 256;
 
 // Byte offsets inside the workspace.
 struct FewWorkspace {
-  size_t plan;   // int32 [kFewPlanWords] the rows of every expert, from few_up to few_down
+  size_t head;   // int32 [kFewUpAt + kFewUpWords], at 0
   size_t next;   // int32 [1] few_down's next item
   size_t done;   // int32 [blocks of 16 output columns] finished parts
   size_t h;      // hidden rows by expert and chunk of columns (few.cu, hidden_at)
@@ -32,7 +34,7 @@ struct FewArgs {
   float* gate;
   int32_t* counts;  // NULL: not wanted
   float* aux;       // NULL: not wanted
-  int32_t* plan;
+  int32_t* head;
   int32_t* next;
   int32_t* done;
   void* h;
@@ -40,6 +42,12 @@ struct FewArgs {
   int split;        // parts that y has room for
   int down_blocks;  // few_down's grid, set by the launcher
   int likely;       // nearly every expert will get tokens, set by the launcher
+  // MOE_DEV_* bits go to *status. The call's own word (head[0]) is cleared by
+  // few_up's first block, and no other knows when: what a wait there that gave up
+  // has OR-ed in may be lost. So each block of few_up then keeps its bits in a
+  // word of the head as well, and few_down, which starts when all of that is
+  // done, adds them.
+  int own;          // 1: the status word is the call's own; set to few_up's grid by the launcher
   int32_t* status;
   uint64_t limit_ns;
 };

@@ -7,7 +7,7 @@ from dataclasses import dataclass
 import torch
 
 from . import _binding as B
-from ._call import check, cuda, device_status, dtype_code, need, on, record
+from ._call import check, cuda, dtype_code, need, on, record
 
 _args = record(22)
 
@@ -17,9 +17,16 @@ class FewOutputs:
     out: torch.Tensor  # [T, d] in x's dtype
     topk_idx: torch.Tensor  # [T, k] int32
     topk_gate: torch.Tensor  # [T, k] fp32
-    status: torch.Tensor  # [1] int32, MOE_DEV_* bits are OR-ed in
+    workspace: torch.Tensor  # uint8
     counts: torch.Tensor | None = None  # [E] int32, when given
     aux: torch.Tensor | None = None  # [1] fp32, when given
+    given_status: torch.Tensor | None = None
+
+    @property
+    def status(self) -> torch.Tensor:
+        """[1] int32, MOE_DEV_* bits: the word that was given, into which this call OR-ed its own, or this call's
+        alone, the workspace's first four bytes (until the next call with this workspace)."""
+        return self.workspace[:4].view(torch.int32) if self.given_status is None else self.given_status
 
 
 def few_workspace_size(T: int, d: int, E: int, k: int, I: int, dtype: torch.dtype) -> int:
@@ -37,8 +44,9 @@ def moe_forward_few(x, w_router, b_router, w_gate, w_up, w_down, k: int, renorm:
     two kernels, with the output in x's dtype. ``counts`` ([E] int32) and
     ``aux`` ([1] fp32) are filled when given. ``workspace``: uint8,
     ``few_workspace_size`` bytes, one for each call that may run at the same
-    time (default: a new one). ``status``: [1] int32 (default:
-    ``device_status`` of the device)."""
+    time (default: a new one). ``status``: [1] int32, into which the call's bits
+    are OR-ed; without it the call's word is the workspace's first four bytes
+    (cleared by the call)."""
     dev = cuda("x", x)
     dt = x.dtype
     code = dtype_code(dt)
@@ -57,9 +65,7 @@ def moe_forward_few(x, w_router, b_router, w_gate, w_up, w_down, k: int, renorm:
         need("counts", counts, torch.int32, (E,), dev)
     if aux is not None:
         need("aux", aux, torch.float32, (1,), dev)
-    if status is None:
-        status = device_status(dev)
-    else:
+    if status is not None:
         need("status", status, torch.int32, (1,), dev)
     lib = B.load_library()
     with on(dev, stream) as s:
@@ -83,5 +89,6 @@ def moe_forward_few(x, w_router, b_router, w_gate, w_up, w_down, k: int, renorm:
             x.data_ptr(), w_router.data_ptr(), 0 if b_router is None else b_router.data_ptr(), w_gate.data_ptr(),
             w_up.data_ptr(), w_down.data_ptr(), T, d, E, k, I, 1 if renorm else 0, code, out.data_ptr(),
             topk_idx.data_ptr(), topk_gate.data_ptr(), 0 if counts is None else counts.data_ptr(),
-            0 if aux is None else aux.data_ptr(), workspace.data_ptr(), workspace.numel(), status.data_ptr(), s)), lib)
-    return FewOutputs(out, topk_idx, topk_gate, status, counts, aux)
+            0 if aux is None else aux.data_ptr(), workspace.data_ptr(), workspace.numel(),
+            workspace.data_ptr() if status is None else status.data_ptr(), s)), lib)
+    return FewOutputs(out, topk_idx, topk_gate, workspace, counts, aux, status)

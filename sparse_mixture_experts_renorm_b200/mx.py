@@ -127,7 +127,7 @@ def mx_matmul(a: MXTensor, b: MXTensor, offsets=None, *, out_dtype=torch.bfloat1
     K] without; ``b`` [N, K] or [groups, N, K], N % 8 == 0. The result is [M, N]
     or [groups, M, N] in ``out_dtype`` (bf16 or fp32); rows of no group are left
     as they are. ``status``: [1] int32, MOE_DEV_* bits are OR-ed in (default:
-    ``device_status`` of the device)."""
+    ``device_status``, one word for all such calls on the device)."""
     if not isinstance(a, MXTensor):
         raise TypeError("a must be an MXTensor")
     dev = cuda("a.data", a.data)

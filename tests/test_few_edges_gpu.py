@@ -4,7 +4,8 @@ import numpy as np
 import pytest
 import torch
 
-from sparse_mixture_experts_renorm_b200 import moe_forward_few
+from sparse_mixture_experts_renorm_b200 import _binding as B
+from sparse_mixture_experts_renorm_b200 import device_status, few_workspace_size, moe_forward_few
 from test_few_gpu import BF16, F32, check_out, check_routing, f64, layer
 
 pytestmark = pytest.mark.gpu
@@ -76,3 +77,34 @@ def test_many_more_items_than_the_joins_may_lie_behind(dtype):
     check_out(p, r.topk_idx, r.topk_gate, r.out, dtype)
     for _ in range(5):
         assert torch.equal(r.out, moe_forward_few(**p, k=k, renorm=True).out)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_a_call_without_a_status_word_has_its_own(dtype):
+    p = layer(5, 256, 8, 2, 64, 53, dtype)
+    q = dict(p, x=p["x"].clone())
+    q["x"][2, 9] = float("nan")
+    device_status("cuda").zero_()
+    bad = moe_forward_few(**q, k=2, renorm=True)
+    good = moe_forward_few(**p, k=2, renorm=True)
+    again = moe_forward_few(**q, k=2, renorm=True)
+    assert [int(r.status) for r in (bad, good, again)] == [B.MOE_DEV_NONFINITE, 0, B.MOE_DEV_NONFINITE]
+    ws = torch.full((few_workspace_size(5, 256, 8, 2, 64, dtype),), 0xFF, dtype=torch.uint8, device="cuda")
+    assert int(moe_forward_few(**p, k=2, renorm=True, workspace=ws).status) == 0
+    assert int(moe_forward_few(**q, k=2, renorm=True, workspace=ws).status) == B.MOE_DEV_NONFINITE
+    # a word that is given keeps what it holds
+    word = torch.full((1,), 64, dtype=torch.int32, device="cuda")
+    r = moe_forward_few(**q, k=2, renorm=True, workspace=ws, status=word)
+    assert r.status is word and int(word) == 64 | B.MOE_DEV_NONFINITE
+    # captured, each replay has its own answer; a graph needs no word made before
+    x = q["x"].clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        r = moe_forward_few(**dict(p, x=x), k=2, renorm=True)
+    for src, want in ((q, B.MOE_DEV_NONFINITE), (p, 0), (q, B.MOE_DEV_NONFINITE)):
+        x.copy_(src["x"])
+        g.replay()
+        assert int(r.status) == want
+    none = moe_forward_few(**dict(p, x=p["x"][:0]), k=2, renorm=True, workspace=ws.fill_(0xFF))
+    assert int(none.status) == 0
+    assert int(device_status("cuda").item()) == 0

@@ -50,3 +50,8 @@ def test_python_refuses_host_tensors():
     w = torch.zeros((4, 64, 64))
     with pytest.raises(ValueError, match="CUDA"):
         moe_forward_few(x, torch.zeros((4, 64)), None, w, w, w, 2, True)
+
+
+def test_the_workspace_as_status_word_needs_room_for_it(lib):
+    st = lib.moe_forward_few(P, P, None, P, P, P, 0, 64, 4, 2, 64, 1, B.MOE_BF16, P, P, P, None, None, P, 3, P, None)
+    assert st == B.MOE_ERR_WORKSPACE and "status" in B.last_error_detail(lib)
