@@ -152,12 +152,12 @@ def mx_matmul(a: MXTensor, b: MXTensor, offsets=None, *, out_dtype=torch.bfloat1
         if q.scales.numel() < _need_scales(g, rows, K, ragged):
             raise ValueError(f"{name}.scales holds {q.scales.numel()} bytes, "
                              f"{_need_scales(g, rows, K, ragged)} are needed")
-    if status is None:
-        status = device_status(dev)
-    else:
+    if status is not None:
         need("status", status, torch.int32, (1,), dev)
     shape = (*sa[:-1], N)
     with on(dev, stream) as s:
+        if status is None:
+            status = device_status(dev)
         if out is None:
             out = a.data.new_empty(shape, dtype=out_dtype)
         else:

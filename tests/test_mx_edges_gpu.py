@@ -7,8 +7,8 @@ import pytest
 import torch
 
 import mx_oracle as O
-from sparse_mixture_experts_renorm_b200 import mx_experts
-from test_mx_gpu import F32, check_experts, experts64, layer
+from sparse_mixture_experts_renorm_b200 import _call, mx_experts, mx_matmul, mx_quantize
+from test_mx_gpu import F32, check_experts, experts64, layer, rand
 
 pytestmark = pytest.mark.gpu
 
@@ -95,3 +95,27 @@ def test_a_row_with_an_infinite_block_keeps_its_other_blocks(T):
     # bf16 on the other; 1.02 for taking the rounded value in place of the value
     tol = (2 * 2.0**-8 + 2.0**-11) * b.abs() + 2.0**-25 * want.double().abs().amax(1, keepdim=True)
     assert ((a - b).abs() <= tol * 1.02).all()
+
+
+@pytest.mark.parametrize("inside", [True, False])
+def test_the_first_product_on_a_device_is_not_captured(inside, monkeypatch):
+    """The device's status word would belong to the graph: refused on a capturing stream, be it torch's current one or
+    the one that is given, and the capture goes on."""
+    a, b = mx_quantize(rand((9, 64), 60)), mx_quantize(rand((16, 64), 61))
+    want, st = mx_matmul(a, b), torch.zeros((1,), dtype=torch.int32, device="cuda")
+    out = torch.zeros_like(want)
+    monkeypatch.setattr(_call, "_status", {})
+    s, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        g.capture_begin()
+        try:
+            with torch.cuda.stream(s if inside else torch.cuda.default_stream()):
+                with pytest.raises(RuntimeError, match="captured"):
+                    mx_matmul(a, b, stream=None if inside else s)
+                mx_matmul(a, b, out=out, status=st, stream=None if inside else s)
+        finally:
+            g.capture_end()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and int(st) == 0
