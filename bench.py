@@ -24,6 +24,7 @@ import argparse
 import hashlib
 import json
 import os
+import re
 import subprocess
 import sys
 import tempfile
@@ -54,18 +55,37 @@ def load_peaks():
     return dict(FALLBACK_PEAKS), "fallback"
 
 
+def device_sources(name):
+    """A kernel's source file and the .cuh headers with device code that it
+    includes, directly or through one another."""
+    csrc = os.path.join(ROOT, "sparse_mixture_experts_renorm_b200", "csrc")
+    found, todo = [], [name]
+    while todo:
+        path = os.path.join(csrc, todo.pop(0))
+        if path in found:
+            continue
+        found.append(path)
+        with open(path) as f:
+            todo += re.findall(r'^#include "(\w+\.cuh)"', f.read(), re.M)
+    return found
+
+
 def source_hash(kernel):
-    src = os.path.join(ROOT, "sparse_mixture_experts_renorm_b200", "csrc", KERNEL_SOURCES[kernel])
-    if not os.path.exists(src):
+    """Of all device code that the kernel is compiled from."""
+    h = hashlib.sha256()
+    try:
+        for path in device_sources(KERNEL_SOURCES[kernel]):
+            with open(path, "rb") as f:
+                h.update(f.read())
+    except OSError:
         return None
-    with open(src, "rb") as f:
-        return hashlib.sha256(f.read()).hexdigest()[:16]
+    return h.hexdigest()[:16]
 
 
 def load_traffic(workload, kernel):
     """DRAM bytes per launch (dram__bytes_read.sum + dram__bytes_write.sum)
     from a committed ncu summary under profiles/, if it was taken on the
-    current source of that kernel; else None."""
+    current source of that kernel, its device headers among it; else None."""
     d = os.path.join(ROOT, "profiles")
     if not os.path.isdir(d):
         return None

@@ -119,3 +119,32 @@ def test_traffic_lookup():
     if v is None:
         pytest.skip("gemm_tc2.cu changed since the committed capture: traffic is reported as null")
     assert 2.0e9 < v < 3.0e9  # about the 2.18 GB of algorithmic bytes
+
+
+def test_the_committed_captures_are_of_the_current_gemm_sources():
+    """Each GEMM slot that a workload launches has its DRAM bytes (at 32 tokens one launch serves both projections)."""
+    for name, kernels in (("mixtral_prefill", 2), ("mixtral_decode", 1), ("small_bf16", 2), ("fine_grained", 2)):
+        for kernel in ("grouped_gemm_gateup_swiglu", "grouped_gemm_down")[:kernels]:
+            v = bench.load_traffic(name, kernel)
+            assert v is not None, f"{name} {kernel}: capture its DRAM bytes again, its source has changed"
+            assert 1e8 < v < 3e9
+
+
+def test_a_changed_header_changes_the_source_hash(tmp_path, monkeypatch):
+    """A helper may move between a kernel's file and its headers: all of its device code is in the hash."""
+    csrc = tmp_path / "sparse_mixture_experts_renorm_b200" / "csrc"
+    csrc.mkdir(parents=True)
+    for path in bench.device_sources("gemm_tc2.cu"):
+        (csrc / os.path.basename(path)).write_bytes(open(path, "rb").read())
+    names = sorted(p.name for p in csrc.iterdir())
+    assert names == ["common.cuh", "gemm_tc2.cu", "pair.cuh"]
+    want = bench.source_hash("grouped_gemm_down")
+    monkeypatch.setattr(bench, "ROOT", str(tmp_path))
+    assert bench.source_hash("grouped_gemm_down") == want
+    for n in names:
+        text = (csrc / n).read_text()
+        (csrc / n).write_text(text + "\n// more\n")
+        assert bench.source_hash("grouped_gemm_down") != want
+        (csrc / n).write_text(text)
+    (csrc / "pair.cuh").unlink()
+    assert bench.source_hash("grouped_gemm_down") is None
