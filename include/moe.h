@@ -413,7 +413,9 @@ size_t moe_mx_scale_bytes(int groups, int rows, int cols, int ragged);
  * the scale of a block is 2^s, s = max(floor(log2(largest magnitude)) - 2,
  * -127), and each element x / 2^s rounded to the nearest code (ties to even,
  * beyond 6 to 6). A block with a NaN or an infinity gets the scale NaN.
- * moe_mx_dequantize — the values back (exact in both types).
+ * moe_mx_dequantize — the values back, exact in both types up to their largest
+ * number; at the scales 2^126 and 2^127, which moe_mx_quantize does not write,
+ * those of 2^128 and more are infinite.
  */
 moe_status moe_mx_quantize(const void* x, const int32_t* offsets, int groups, int rows, int cols, moe_dtype dtype,
                            void* data, void* scales, size_t scale_bytes, void* stream);

@@ -95,7 +95,8 @@ def mx_quantize(x, offsets=None, *, stream=None) -> MXTensor:
 
 
 def mx_dequantize(q: MXTensor, dtype=torch.bfloat16, offsets=None, *, out=None, stream=None) -> torch.Tensor:
-    """The values of ``q`` in ``dtype`` (bf16 or fp32: exact in both). With
+    """The values of ``q`` in ``dtype`` (bf16 or fp32: exact in both, infinite
+    from 2^128 on, which only scales that ``mx_quantize`` does not write reach). With
     ``offsets`` as given to ``mx_quantize``; rows of no group are left as they
     are in ``out`` (unset in a new one)."""
     if not isinstance(q, MXTensor):

@@ -7,8 +7,8 @@ import pytest
 import torch
 
 import mx_oracle as O
-from sparse_mixture_experts_renorm_b200 import _call, mx_experts, mx_matmul, mx_quantize
-from test_mx_gpu import F32, check_experts, experts64, layer, rand
+from sparse_mixture_experts_renorm_b200 import MXTensor, _call, mx_dequantize, mx_experts, mx_matmul, mx_quantize
+from test_mx_gpu import BF16, F32, check_experts, experts64, layer, rand
 
 pytestmark = pytest.mark.gpu
 
@@ -119,3 +119,21 @@ def test_the_first_product_on_a_device_is_not_captured(inside, monkeypatch):
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want) and int(st) == 0
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_every_code_at_every_scale(dtype):
+    """Exact from 2^-128 (0.5 at the smallest scale, subnormal) up to 1.5 2^127; what passes that, at the scales 2^126
+    and 2^127, is infinite, and the scale 0xFF is NaN."""
+    code = torch.arange(16, dtype=torch.uint8)
+    row = code[0::2] | code[1::2] << 4  # the 16 codes, and again
+    data = row.repeat(2).repeat(256, 1).cuda()
+    scales = torch.zeros((2048,), dtype=torch.uint8)
+    r = torch.arange(256)
+    scales[r // 128 * 1024 + r % 32 * 16 + r % 128 // 32 * 4] = r.to(torch.uint8)
+    got = mx_dequantize(MXTensor(data, scales.cuda()), dtype).cpu().double()
+    level = torch.tensor([0, 0.5, 1, 1.5, 2, 3, 4, 6, -0.0, -0.5, -1, -1.5, -2, -3, -4, -6], dtype=torch.float64).repeat(2)
+    want = level * torch.exp2(r[:255, None].double() - 127)
+    want = torch.where(want.abs() >= 2.0**128, torch.sign(want) * float("inf"), want)
+    assert torch.equal(got[:255], want) and torch.equal(torch.signbit(got[:255]), torch.signbit(want))
+    assert torch.isnan(got[255]).all()
