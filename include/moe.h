@@ -373,8 +373,10 @@ moe_status moe_pipeline_destroy(moe_pipeline* p);
  *   workspace   moe_few_workspace_size() bytes, 256-byte aligned, any contents;
  *               calls that overlap on the GPU need one each
  * MOE_BF16: d % 8 == 0 and I % 8 == 0; MOE_F32: d % 4 == 0 and I % 4 == 0.
- * Experts rank by their logits (as their exact probabilities do). Results are
- * bit-identical from run to run.
+ * Products and sums are fp32. For MOE_BF16 the hidden values are kept in two
+ * bf16 terms (2^-16 of a value), and SiLU takes the fast exponential and
+ * division (2^-18). Experts rank by their logits (as their exact probabilities
+ * do). Results are bit-identical from run to run.
  */
 #define MOE_FEW_TOKENS 16
 size_t moe_few_workspace_size(int T, int d, int E, int k, int I, moe_dtype dtype);
@@ -443,8 +445,13 @@ moe_status moe_mx_matmul(const void* a, const void* a_scales, const void* b, con
  * and the SwiGLU hidden rows are rounded to MXFP4 from fp32 between them. Each
  * expert row times its gate is rounded to 2^-11 of a value (2^-25 of the
  * largest of its 32 columns where that is more), a token's rows are added in slot order in fp32, and out
- * [T, d] is bf16. d % 32 == 0 and I % 32 == 0; E I, E d and T k at most
+ * [T, d] is bf16, for fp32 x as well. SiLU takes the fast exponential and
+ * division (2^-18). d % 32 == 0 and I % 32 == 0; E I, E d and T k at most
  * 2^31 - 256, d I below 2^31.
+ * What four bits cost: on normally distributed data, whatever the sizes, MXFP4
+ * leaves a matrix 0.11 of its norm off; the layer's output is 0.20 of its norm
+ * off by the weights' rounding alone, and 0.30 with that of x and the hidden
+ * rows, which these functions also round.
  *
  * moe_mx_experts takes the choices and gates: topk_idx [T, k], any experts
  * (the same one twice is two assignments), topk_gate [T, k] any values. A

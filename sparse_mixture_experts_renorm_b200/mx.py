@@ -247,7 +247,9 @@ def mx_experts(x, topk_idx, topk_gate, w_gate: MXTensor, w_up: MXTensor, w_down:
     [E, I, d], [E, I, d] and [E, d, I]. out[t] = sum_j gate[t, j] y of expert
     idx[t, j], bf16. ``workspace``: uint8, ``mx_workspace_size`` bytes, one for
     each call that may run at the same time. Without ``status`` the call's word
-    is the workspace's first four bytes (cleared by the call)."""
+    is the workspace's first four bytes (cleared by the call). x and the hidden
+    rows are rounded to MXFP4 too: on normal data ``out`` is 0.30 of its norm
+    off, of which the weights alone would make 0.20 (include/moe.h)."""
     dev, dt = _rows(x)
     T, d = x.shape
     w, E, I = _weights(w_gate, w_up, w_down, dev, d)

@@ -126,3 +126,22 @@ def test_oracle_rounds_to_the_nearest_code():
     one[0, :9] = [4, 0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5, 100]  # ties to the even code; 100 sets the scale
     assert O.values(O.round_codes(one, np.zeros((1, 1), int)), np.zeros((1, 1), int))[0, :9].tolist() == [
         4, 0, 1, 1, 2, 2, 4, 4, 6]
+
+
+@pytest.mark.parametrize("d,I", [(128, 160), (1024, 512)])
+def test_what_four_bits_cost_on_normal_data(d, I):
+    """The figures of include/moe.h, from the definition: 0.11 of a matrix's norm, 0.20 of the layer's output by the
+    weights alone, 0.30 with x and the hidden rows rounded as well."""
+    r = np.random.default_rng(1)
+    x = r.standard_normal((64, d))
+    w = [r.standard_normal(s) * 0.02 for s in ((I, d), (I, d), (d, I))]
+
+    def layer(x, wg, wu, wd, keep):
+        g = x @ wg.T
+        return keep(g / (1 + np.exp(-g)) * (x @ wu.T)) @ wd.T
+
+    want, q = layer(x, *w, lambda h: h), [O.fake(v) for v in w]
+    off = lambda a, b: np.linalg.norm(a - b) / np.linalg.norm(b)  # noqa: E731
+    assert 0.105 < off(q[0], w[0]) < 0.12
+    assert 0.18 < off(layer(x, *q, lambda h: h), want) < 0.22
+    assert 0.27 < off(layer(O.fake(x), *q, O.fake), want) < 0.32
