@@ -440,9 +440,17 @@ cudaError_t launch(const MxMaps& m, const int32_t* offsets, int G, int M, int N,
 
 cudaError_t launch_mx_product(const MxMaps& m, const int32_t* offsets, int G, int M, int N, int K, int group_tiles,
                               const MxOut& out, int32_t* status, cudaStream_t stream) {
-  // 64 groups of N 1408, K 2048, us there and here: 8 rows each on average 20.6
-  // and 22.7, 32 rows 22.0 and 24.1, 64 rows 24.9 and 26.0, 96 rows 27.5 and 27.5,
-  // 128 rows 30.6 and 28.1
+  // By the average, as the lengths are known only on the device. us there and
+  // here, in a graph, weights from memory:
+  //   rows in every group       8           64          96          128         192
+  //   64 x 1408 x 2048      22.5 24.4   25.2 26.0   26.7 27.4   28.0 28.3   39.8 30.1
+  //   8 x 4096 x 14336      46.5 51.0   45.4 49.8   46.3 50.9   47.2 51.7   62.8 53.5
+  //   8 x 14336 x 4096      49.1 55.4   49.5 57.3   50.5 58.4   52.2 59.2   74.4 61.0
+  //   1 x 4096 x 4096        8.7 11.3    9.2 10.5    9.2 10.9    9.2 11.1    9.6 11.3
+  // Its tiles hold 128 rows, so groups of equal length cross between 128 and 192.
+  // Uneven ones do before, and half of that leaves room for them: 64 groups of 60
+  // rows on average, the largest of 809, 26.7 and 26.0; one of 4000 rows among 63
+  // of one, 29.9 and 28.8 (K 1408, N 2048: 32.8 and 30.6, the worst that was seen)
   if ((long long)M <= (offsets ? 64ll * G : 64ll))
     return launch_mx_product_rows(m, offsets, G, M, N, K, group_tiles, out, status, stream);
   if (out.form == kMxY16) return launch<kMxY16>(m, offsets, G, M, N, K, group_tiles, out, status, stream);

@@ -14,8 +14,8 @@
 // tile's products. 26 KB a stage, 8 stages; otherwise as there.
 //
 // Taken where groups have at most 64 rows on average (mx_gemm.cu has both sides
-// measured: with more, twice the tiles and stores of single columns cost what
-// the rows save). Bound by the weights' bytes: 64 rows over 8 groups of 4096 x
+// measured: past 128 rows a group takes twice the tiles, and stores of single
+// columns). Bound by the weights' bytes: 64 rows over 8 groups of 4096 x
 // 14336 in 46 us, 5.4 TB/s, with the weights in memory (40 us when the call is
 // repeated and L2 still holds a part of them).
 #include "mx_umma.cuh"
