@@ -375,8 +375,9 @@ moe_status moe_pipeline_destroy(moe_pipeline* p);
  * MOE_BF16: d % 8 == 0 and I % 8 == 0; MOE_F32: d % 4 == 0 and I % 4 == 0.
  * Products and sums are fp32. For MOE_BF16 the hidden values are kept in two
  * bf16 terms (2^-16 of a value), and SiLU takes the fast exponential and
- * division (2^-18). Experts rank by their logits (as their exact probabilities
- * do). Results are bit-identical from run to run.
+ * division (2^-18); an output that an infinite down weight takes part in is NaN
+ * or infinite. Experts rank by their logits (as their exact probabilities do).
+ * Results are bit-identical from run to run.
  */
 #define MOE_FEW_TOKENS 16
 size_t moe_few_workspace_size(int T, int d, int E, int k, int I, moe_dtype dtype);
