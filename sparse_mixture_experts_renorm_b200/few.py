@@ -50,7 +50,7 @@ def moe_forward_few(x, w_router, b_router, w_gate, w_up, w_down, k: int, renorm:
     dev = cuda("x", x)
     dt = x.dtype
     code = dtype_code(dt)
-    if x.dim() != 2 or w_gate.dim() != 3:
+    if x.dim() != 2 or not isinstance(w_gate, torch.Tensor) or w_gate.dim() != 3:
         raise ValueError("x must be [T, d] and w_gate [E, I, d]")
     T, d = x.shape
     E, I, _ = w_gate.shape

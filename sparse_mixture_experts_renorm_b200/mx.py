@@ -253,8 +253,8 @@ def mx_experts(x, topk_idx, topk_gate, w_gate: MXTensor, w_up: MXTensor, w_down:
     dev, dt = _rows(x)
     T, d = x.shape
     w, E, I = _weights(w_gate, w_up, w_down, dev, d)
-    if topk_idx.dim() != 2:
-        raise ValueError("topk_idx must be [T, k]")
+    if not isinstance(topk_idx, torch.Tensor) or topk_idx.dim() != 2:
+        raise ValueError("topk_idx must be a [T, k] tensor")
     k = topk_idx.shape[1]
     need("topk_idx", topk_idx, torch.int32, (T, k), dev)
     need("topk_gate", topk_gate, torch.float32, (T, k), dev)

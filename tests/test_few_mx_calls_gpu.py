@@ -203,3 +203,14 @@ def test_few_tokens_with_more_than_2_32_weights():
     r = moe_forward_few(**big, k=1, renorm=True)
     assert r.topk_idx.tolist() == [[E - 1]] * T
     F.check_out(p, torch.zeros_like(r.topk_idx), r.topk_gate, r.out, BF16)
+
+
+def test_what_is_no_tensor_is_refused_as_any_wrong_argument():
+    p = F.layer(4, 128, 8, 2, 64, 105, BF16)
+    x, idx, gate, w = layer(4, 64, 4, 2, 64, 106)
+    for name in ("x", "w_router", "w_gate", "w_up", "w_down", "b_router"):
+        with pytest.raises(ValueError):
+            moe_forward_few(**dict(p, **{name: p[name].tolist()}), k=2, renorm=True)
+    for args in ((x.tolist(), idx, gate), (x, idx.tolist(), gate), (x, idx, gate.tolist())):
+        with pytest.raises(ValueError):
+            mx_experts(*args, *w)
