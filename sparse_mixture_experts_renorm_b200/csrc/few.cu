@@ -25,11 +25,12 @@
 // finished part is written to y, and the last of a block of 16 columns to
 // finish adds them up, in a fixed order whatever the order of arrival.
 //
-// Measured (bf16, us and bytes that it cannot do without over the time): 16
-// tokens of the Mixtral-shaped layer (d 4096, I 14336, 8 experts, k 2) 422 us,
-// 6.6 TB/s; 5 tokens of the fine-grained one (d 2048, I 1408, 64 experts, k 6)
-// 76 us, 5.7 TB/s; one token of the small one (d 1024, I 2816, 8 experts, k 2)
-// 20 us, 1.7 TB/s. What is left there: some 8 us from the launch to the first
+// Measured (bf16, in a graph, us and bytes that it cannot do without over the
+// time): 16 tokens of the Mixtral-shaped layer (d 4096, I 14336, 8 experts, k 2)
+// 424 to 437 us between boxes, 6.4 to 6.6 TB/s (called one by one 438 to 470 us);
+// 5 tokens of the fine-grained one (d 2048, I 1408, 64 experts, k 6) 76 us, 5.7
+// TB/s; one token of the small one (d 1024, I 2816, 8 experts, k 2) 20.5 us, 1.7
+// TB/s. What is left there: some 8 us from the launch to the first
 // weight (3.6 us of logits, 2.5 us of choosing and 1.3 us of grouping for 64
 // experts; half of that for 8), 4 us between the kernels, and the last items'
 // and joins' tail.

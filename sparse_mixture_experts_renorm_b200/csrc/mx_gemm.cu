@@ -32,8 +32,8 @@
 // Persistent: clusters walk the tiles (groups in order, weight block outer,
 // row tile inner). Every wait is bounded.
 //
-// Measured: 8192 x 14336 x 4096 to bf16 in 164 us, 5.9 PFLOP/s (a burst; the
-// tensor pipe is busy 77 % of the time). Run for seconds it draws the 1 kW that
+// Measured: 8192 x 14336 x 4096 to bf16 in 161 to 169 us, 5.9 PFLOP/s (bursts;
+// the tensor pipe is busy 79 % of the time). Run for seconds it draws the 1 kW that
 // the card allows, the clock falls from 1.9 to 1.4 GHz and it takes 195 us;
 // with zeros for codes it does not. A tile costs 0.9 us beside its products
 // (the last of them, the accumulator's way out, the first stage): 28 % for the

@@ -62,7 +62,6 @@ bool make_tmap_mx_scales(CUtensorMap* map, const void* base, uint64_t rows);
 // counts of every expert, the rank of every (token, slot) among the block's
 // assignments of its expert (slots of a token in order), and zeros in
 // blk_psum. A choice outside [0, E) sets MOE_DEV_INTERNAL and gets rank -1.
-// clear_status: the word is the call's own and is cleared first.
 cudaError_t launch_mx_count(const int32_t* topk_idx, int T, int E, int k, int32_t* lrank, int32_t* blk_cnt,
                             float* blk_psum, int32_t* status, cudaStream_t stream);
 
