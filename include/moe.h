@@ -445,10 +445,11 @@ moe_status moe_mx_matmul(const void* a, const void* a_scales, const void* b, con
  * router sees x itself), both products of an expert multiply MXFP4 matrices,
  * and the SwiGLU hidden rows are rounded to MXFP4 from fp32 between them. Each
  * expert row times its gate is rounded to 2^-11 of a value (2^-25 of the
- * largest of its 32 columns where that is more), a token's rows are added in slot order in fp32, and out
- * [T, d] is bf16, for fp32 x as well. SiLU takes the fast exponential and
- * division (2^-18). d % 32 == 0 and I % 32 == 0; E I, E d and T k at most
- * 2^31 - 256, d I below 2^31.
+ * largest of its 32 columns where that is more; bf16's 2^-8 in 32 columns with
+ * a NaN or an infinity among them), a token's rows are added in slot order in
+ * fp32, and out [T, d] is bf16, for fp32 x as well. SiLU takes the fast
+ * exponential and division (2^-18). d % 32 == 0 and I % 32 == 0; E I, E d and
+ * T k at most 2^31 - 256, d I below 2^31.
  * What four bits cost: on normally distributed data, whatever the sizes, MXFP4
  * leaves a matrix 0.11 of its norm off; the layer's output is 0.20 of its norm
  * off by the weights' rounding alone, and 0.30 with that of x and the hidden
@@ -461,8 +462,9 @@ moe_status moe_mx_matmul(const void* a, const void* a_scales, const void* b, con
  * moe_mx_forward runs the router before them; arguments and outputs as for
  * moe_forward (x and w_router in `dtype`, with the limits of its router).
  * workspace: moe_mx_workspace_size() bytes, 256-byte aligned, any contents;
- * calls that overlap on the GPU need one each.
- * Results are bit-identical from run to run.
+ * calls that overlap on the GPU need one each. status_dev: MOE_DEV_* bits are
+ * OR-ed in; NULL: the call's own word, the workspace's first four bytes, cleared
+ * by the call. Results are bit-identical from run to run.
  */
 typedef struct moe_mx_weights {
   size_t struct_bytes;      /* sizeof(moe_mx_weights) */
